@@ -1,4 +1,4 @@
-"""B200-native DCKV codec: Python binding of the C ABI in include/dckv.h.
+"""B200-native DCKV codec: Python binding of the C ABI in include/*.h.
 
 The binding only marshals arguments: every step of encode and decode runs in the
 CUDA library ``libdckv_b200.so`` (sm_100a).  PyTorch supplies device memory and
@@ -35,6 +35,12 @@ FIT_OFF_CO = FIT_OFF_GO + 6144 * 6144
 FIT_OFF_N = FIT_OFF_CO + 6144 * 2048
 FIT_STATS_DOUBLES = FIT_OFF_N + 8
 
+# element types, rotary layouts, scalings and modes (include/dckv_cache.h)
+DCKV_BF16, DCKV_FP16, DCKV_FP32 = range(3)
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+ROPE_MODES = {"forward": 0, "gradient": 1, "inverse": 2}
+
 _lib = None
 
 
@@ -65,6 +71,40 @@ class WsView(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in ("q32", "qe", "cen8", "row_slot", "sym16", "q16", "x16", "g16", "counters")] + [
         ("n_rows", ctypes.c_int64), ("ne_pad", ctypes.c_int64), ("n_chunks", ctypes.c_int32),
         ("total", ctypes.c_uint64), ("code_width", ctypes.c_int32)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", ctypes.c_double),
+                ("freq", ctypes.c_double * 128)]
+
+
+class KvPool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("device", "dtype", "n_layers", "n_kv_heads", "head_dim", "page_size")] + [
+        (n, ctypes.c_int64) for n in ("n_pages", "k_layer_stride", "k_page_stride", "k_row_stride", "k_head_stride",
+                                      "v_layer_stride", "v_page_stride", "v_row_stride", "v_head_stride")]
+
+
+class CacheBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "max_new", "max_pages", "reserved")] + [
+        (n, ctypes.c_void_p) for n in ("offsets", "kv_lens", "page_table")] + [("table_stride", ctypes.c_int64)]
+
+
+class _AppendArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("k_layer_stride", "k_token_stride", "k_head_stride", "v_layer_stride",
+                                      "v_token_stride", "v_head_stride")] + [
+        ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride", "q_out_token_stride", "q_out_head_stride",
+                                      "n_tokens")] + [
+        ("n_q_heads", ctypes.c_int32), ("reserved", ctypes.c_int32), ("positions", ctypes.c_void_p)]
+
+
+class _AttentionArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "out", "lse")] + [
+        (n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride", "out_token_stride", "out_head_stride",
+                                      "n_tokens")] + [
+        (n, ctypes.c_int32) for n in ("n_q_heads", "layer", "causal")] + [("scale", ctypes.c_float)]
 
 
 def lib():
@@ -104,6 +144,13 @@ def lib():
         "dckv_fit_to_bf16": (I, [P, ctypes.c_int64, P, P]),
         "dckv_fit_scales_accumulate": (I, [P, P, P, P, I, P, P, P, Z, P]),
         "dckv_fit_scales_finish": (I, [P, P, P, P]),
+        "dckv_rope_init": (I, [P, I, I, ctypes.c_double, I] + [ctypes.c_double] * 5),
+        "dckv_rope": (I, [P, I, I, I, P, ctypes.c_int64, ctypes.c_int64, P, ctypes.c_int64, ctypes.c_int64,
+                          ctypes.c_int64, I, I, P, P]),
+        "dckv_cache_append": (I, [P, P, P, P, P, P]),
+        "dckv_cache_rows": (I, [P, P, P, P, ctypes.c_int64, ctypes.c_int64, P, P, P]),
+        "dckv_attention_workspace_bytes": (Z, [P, P, I]),
+        "dckv_attention": (I, [P, P, P, P, P, Z, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -329,6 +376,208 @@ def dckv_fit_scales_finish(handle, abs_sum, laplace_b, stream=None):
            "dckv_fit_scales_finish")
 
 
+# ---------------------------------------------------- paged cache and attention (dckv_cache.h)
+def _bad(what):
+    raise DckvError(DCKV_EINVAL, what)
+
+
+def _dtype_code(t):
+    import torch
+
+    code = {torch.bfloat16: DCKV_BF16, torch.float16: DCKV_FP16, torch.float32: DCKV_FP32}.get(t.dtype)
+    if code is None:
+        _bad(f"type {t.dtype} is not supported")
+    return code
+
+
+def _cuda_check(device, **tensors):
+    """Every tensor given sits on CUDA device `device` with a contiguous last dimension."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or t.device.index != device:
+            _bad(f"{name} is on {t.device}, not on cuda:{device}")
+        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            _bad(f"the last dimension of {name} must be contiguous")
+
+
+def _int32_check(**tensors):
+    import torch
+
+    for name, t in tensors.items():
+        if t is not None and t.dtype != torch.int32:
+            _bad(f"{name} must be int32, not {t.dtype}")
+
+
+def _device_stream(device, stream):
+    """The given stream, or the current one of that device (not of the current device)."""
+    import torch
+
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def rope_spec(rotary_dim, layout="half", base=1.0e7, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=32.0,
+              magnitude=1.0) -> RopeSpec:
+    """A rotation (dckv_rope_init): layout "half" or "interleaved"; scaling "none", "linear",
+    "ntk" or "parts".  The codec's own is rope_spec(256)."""
+    for what, name, known in (("layout", layout, ROPE_LAYOUTS), ("scaling", scaling, ROPE_SCALINGS)):
+        if name not in known:
+            _bad(f"unknown rotary {what} {name!r}")
+    s = RopeSpec()
+    _check(lib().dckv_rope_init(ctypes.byref(s), int(rotary_dim), ROPE_LAYOUTS[layout], float(base),
+                                ROPE_SCALINGS[scaling], float(factor), float(original_len), float(low), float(high),
+                                float(magnitude)), "dckv_rope_init")
+    return s
+
+
+def dckv_rope(spec, x, positions, out, mode="forward", stream=None):
+    """Rotates x [n, heads, dim] (bf16, fp16 or fp32) by positions int32 [n] into out (which may
+    be x).  mode "forward", "gradient" (the transpose) or "inverse"."""
+    if mode not in ROPE_MODES:
+        _bad(f"unknown rotary mode {mode!r}")
+    if x.dim() != 3 or out.shape != x.shape or positions.shape != x.shape[:1]:
+        _bad("x and out must be [n, heads, dim] alike and positions [n]")
+    if out.dtype != x.dtype:
+        _bad("out must have x's type")
+    dev = x.device.index
+    _cuda_check(dev, x=x, out=out, positions=positions)
+    _int32_check(positions=positions)
+    n, heads, dim = x.shape
+    if n == 0:
+        return out
+    xs, os_ = x.stride(), out.stride()
+    _check(lib().dckv_rope(ctypes.byref(spec), ROPE_MODES[mode], dev, _dtype_code(x), x.data_ptr(), xs[0], xs[1],
+                           out.data_ptr(), os_[0], os_[1], n, heads, dim, positions.data_ptr(),
+                           _device_stream(dev, stream)), "dckv_rope")
+    return out
+
+
+def kv_pool(k, v) -> KvPool:
+    """Describes page pools k, v [layers, pages, rows, heads, dim] (or one layer's four
+    dimensions), any strides with a contiguous last dimension.  Keeps the tensors alive."""
+    if k.dim() == 4:
+        k, v = k[None], v[None]
+    if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype:
+        _bad("k and v must be [layers, pages, rows, heads, dim] alike")
+    dev = k.device.index
+    _cuda_check(dev, k=k, v=v)
+    ks, vs = k.stride(), v.stride()
+    p = KvPool(k.data_ptr(), v.data_ptr(), dev, _dtype_code(k), k.shape[0], k.shape[3], k.shape[4], k.shape[2],
+               k.shape[1], *ks[:4], *vs[:4])
+    p.tensors = (k, v)
+    return p
+
+
+def cache_batch(offsets, kv_lens, page_table, max_new) -> CacheBatch:
+    """Describes the sequences of a call: int32 offsets [batch + 1], kv_lens [batch] and
+    page_table [batch, pages] on the pool's device; max_new bounds any sequence's new tokens.
+    Keeps the tensors alive; their contents may change between calls (and graph replays)."""
+    if kv_lens.dim() != 1 or offsets.shape != (kv_lens.shape[0] + 1,) or page_table.dim() != 2 or \
+            page_table.shape[0] != kv_lens.shape[0]:
+        _bad("offsets, kv_lens and page_table must be [batch + 1], [batch] and [batch, pages]")
+    dev = offsets.device.index
+    _cuda_check(dev, offsets=offsets, kv_lens=kv_lens, page_table=page_table)
+    _int32_check(offsets=offsets, kv_lens=kv_lens, page_table=page_table)
+    b = CacheBatch(kv_lens.shape[0], int(max_new), page_table.shape[1], 0, offsets.data_ptr(), kv_lens.data_ptr(),
+                   page_table.data_ptr(), page_table.stride(0))
+    b.tensors = (offsets, kv_lens, page_table)
+    b.device = dev
+    return b
+
+
+def _pool_check(pool, batch, status, **tensors):
+    if batch.device != pool.device:
+        _bad(f"the batch is on cuda:{batch.device}, the pool on cuda:{pool.device}")
+    _cuda_check(pool.device, status=status, **tensors)
+    _int32_check(status=status)
+
+
+def dckv_cache_append(pool, batch, k, v, status, rope=None, positions=None, q=None, q_out=None, stream=None):
+    """k, v [layers, n, heads, dim] (or one layer's three dimensions) into the pages, keys rotated
+    by `rope` if given; q [n, q heads, dim] rotated into q_out beside them."""
+    if k.dim() == 3:
+        k, v = k[None], v[None]
+    n = k.shape[1]
+    if k.shape != (pool.n_layers, n, pool.n_kv_heads, pool.head_dim) or v.shape != k.shape:
+        _bad("k and v must be [layers, n, heads, dim] of the pool")
+    if _dtype_code(k) != pool.dtype or v.dtype != k.dtype:
+        _bad("k and v must have the pool's type")
+    _pool_check(pool, batch, status, k=k, v=v, positions=positions, q=q, q_out=q_out)
+    ks, vs = k.stride(), v.stride()
+    a = _AppendArgs(k.data_ptr(), v.data_ptr(), *ks[:3], *vs[:3])
+    a.n_tokens = n
+    if positions is not None:
+        _int32_check(positions=positions)
+        if positions.shape != (n,):
+            _bad("positions must be [n]")
+        a.positions = positions.data_ptr()
+    if q is not None:
+        if q_out is None or q.dim() != 3 or q.shape[0] != n or q.shape[2] != pool.head_dim or q_out.shape != q.shape:
+            _bad("q and q_out must be [n, q heads, dim]")
+        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+            _bad("q and q_out must have the pool's type")
+        a.q, a.q_out, a.n_q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+        a.q_token_stride, a.q_head_stride = q.stride()[:2]
+        a.q_out_token_stride, a.q_out_head_stride = q_out.stride()[:2]
+    elif q_out is not None:
+        _bad("q_out without q")
+    if n == 0:
+        return
+    _check(lib().dckv_cache_append(ctypes.byref(pool), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
+                                   ctypes.byref(a), status.data_ptr(), _device_stream(pool.device, stream)),
+           "dckv_cache_append")
+
+
+def dckv_cache_rows(pool, batch, rows, status, rope=None, positions=None, stream=None):
+    """The sequences' first slots as rows [n, layers * 2 * heads * dim], keys rotated back by
+    `rope` if given."""
+    if rows.dim() != 2 or rows.shape[1] != 2 * pool.n_layers * pool.n_kv_heads * pool.head_dim:
+        _bad("rows must be [n, layers * 2 * heads * dim]")
+    if _dtype_code(rows) != pool.dtype:
+        _bad("rows must have the pool's type")
+    _pool_check(pool, batch, status, rows=rows, positions=positions)
+    if positions is not None:
+        _int32_check(positions=positions)
+        if positions.shape != rows.shape[:1]:
+            _bad("positions must be [n]")
+    if rows.shape[0] == 0:
+        return rows
+    _check(lib().dckv_cache_rows(ctypes.byref(pool), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
+                                 rows.data_ptr(), rows.stride(0), rows.shape[0], _ptr(positions), status.data_ptr(),
+                                 _device_stream(pool.device, stream)), "dckv_cache_rows")
+    return rows
+
+
+def dckv_attention_workspace_bytes(pool, batch, n_q_heads) -> int:
+    n = int(lib().dckv_attention_workspace_bytes(ctypes.byref(pool), ctypes.byref(batch), int(n_q_heads)))
+    if n == 0:
+        _bad(f"dckv_attention_workspace_bytes ({last_error()})")
+    return n
+
+
+def dckv_attention(pool, layer, batch, q, out, status, workspace, scale=None, causal=True, lse=None, stream=None):
+    """Attention of q [n, q heads, dim] over the sequences' slots in `layer` into out (same shape)
+    and, if given, lse fp32 [n, q heads].  scale: dim ** -0.5 unless given."""
+    if q.dim() != 3 or q.shape[2] != pool.head_dim or out.shape != q.shape:
+        _bad("q and out must be [n, q heads, dim]")
+    if _dtype_code(q) != pool.dtype or out.dtype != q.dtype:
+        _bad("q and out must have the pool's type")
+    _pool_check(pool, batch, status, q=q, out=out, lse=lse, workspace=workspace)
+    n = q.shape[0]
+    a = _AttentionArgs(q.data_ptr(), out.data_ptr(), None, *q.stride()[:2], *out.stride()[:2], n, q.shape[1],
+                       int(layer), 1 if causal else 0, pool.head_dim ** -0.5 if scale is None else float(scale))
+    if lse is not None:
+        if lse.shape != q.shape[:2] or _dtype_code(lse) != DCKV_FP32 or not lse.is_contiguous():
+            _bad("lse must be contiguous fp32 [n, q heads]")
+        a.lse = lse.data_ptr()
+    if n == 0:
+        return out
+    _check(lib().dckv_attention(ctypes.byref(pool), ctypes.byref(batch), ctypes.byref(a), status.data_ptr(),
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                _device_stream(pool.device, stream)), "dckv_attention")
+    return out
+
+
 def upload_params(codec, device="cuda"):
     """Device tensors for dckv_codec_create from an object with numpy attributes mu, basis,
     w1, w2, delta, laplace_b (float32), embed, w_even, w_odd (bf16 bits as uint16) and,
@@ -423,3 +672,122 @@ class Codec:
             self.close()
         except Exception:
             pass
+
+
+class PagedCache:
+    """A paged cache beside a codec: owns the page pools, a list of free pages and each
+    sequence's pages and length (on the host), and makes the calls of dckv_cache.h on them.
+
+    A step: ``batch = cache.extend(seqs, counts)`` gives the sequences room for their new tokens;
+    then per layer or at once ``cache.append(batch, k, v, q=q)`` and
+    ``cache.attend(layer, batch, q)``.  ``restore`` and ``store`` move whole prompts between
+    blobs of a Codec and the pages.  Everything runs on the current stream of the cache's device;
+    calls on one cache that overlap in time (two streams) need ordering between them."""
+
+    def __init__(self, n_pages, page_size=64, n_layers=6, n_kv_heads=2, head_dim=256, dtype=None, device=0, rope=None):
+        import torch
+
+        self.torch = torch
+        self.device = torch.device("cuda", device)
+        shape = (n_layers, n_pages, page_size, n_kv_heads, head_dim)
+        self.k = torch.empty(shape, dtype=dtype or torch.bfloat16, device=self.device)
+        self.v = torch.empty_like(self.k)
+        self.pool = kv_pool(self.k, self.v)
+        self.rope = rope_spec(head_dim) if rope is None else rope
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._free = list(range(n_pages - 1, -1, -1))
+        self._pages, self._len = {}, {}
+        self._ws = None
+        self._next = 0
+
+    def add(self) -> int:
+        """A new, empty sequence."""
+        s = self._next
+        self._next += 1
+        self._pages[s], self._len[s] = [], 0
+        return s
+
+    def length(self, seq) -> int:
+        return self._len[seq]
+
+    def drop(self, seq):
+        """Gives a sequence's pages back (work already queued on the current stream still reads
+        them in order)."""
+        self._free += reversed(self._pages.pop(seq))
+        del self._len[seq]
+
+    def _batch(self, seqs, counts):
+        torch = self.torch
+        width = max(1, max(len(self._pages[s]) for s in seqs))
+        table = np.zeros((len(seqs), width), np.int32)
+        for i, s in enumerate(seqs):
+            table[i, : len(self._pages[s])] = self._pages[s]
+        offs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        lens = np.array([self._len[s] for s in seqs], np.int32)
+        dev = [torch.from_numpy(a).to(self.device) for a in (offs, lens, table)]
+        return cache_batch(*dev, max(1, max(counts)))
+
+    def extend(self, seqs, counts) -> CacheBatch:
+        """Room for counts[i] more tokens of seqs[i]; the batch of a call that appends them."""
+        seqs, counts = list(seqs), [int(c) for c in counts]
+        if not seqs or len(seqs) != len(counts) or len(set(seqs)) != len(seqs) or min(counts) < 0:
+            _bad("extend takes different sequences and one count of at least 0 for each")
+        rows = self.pool.page_size
+        need = [-(-(self._len[s] + c) // rows) - len(self._pages[s]) for s, c in zip(seqs, counts)]
+        if sum(need) > len(self._free):
+            raise DckvError(DCKV_ECAPACITY, f"{sum(need)} pages needed, {len(self._free)} free")
+        for s, c, m in zip(seqs, counts, need):
+            self._pages[s] += [self._free.pop() for _ in range(m)]
+            self._len[s] += c
+        return self._batch(seqs, counts)
+
+    def append(self, batch, k, v, q=None, q_out=None, rotate=True, positions=None):
+        """dckv_cache_append with the cache's rotation (rotate=False: keys come rotated)."""
+        dckv_cache_append(self.pool, batch, k, v, self.status, rope=self.rope if rotate else None, positions=positions,
+                          q=q, q_out=q_out)
+
+    def attend(self, layer, batch, q, out=None, scale=None, causal=True, lse=None):
+        """dckv_attention on the cache's workspace; out is a new tensor unless given."""
+        need = dckv_attention_workspace_bytes(self.pool, batch, q.shape[1])
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
+        if out is None:
+            out = self.torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return dckv_attention(self.pool, layer, batch, q, out, self.status, self._ws, scale=scale, causal=causal,
+                              lse=lse)
+
+    def restore(self, codec, blob, blob_bytes, token_ids, seq_offsets):
+        """Decodes a blob's prompts into new sequences of the pages (the decoder rotates the keys
+        as the codec's own rotation does).  Returns the sequences; codec.status has the decoder's
+        status."""
+        counts = [int(c) for c in np.diff(np.asarray(seq_offsets, np.int64))]
+        if min(counts) < 1:
+            _bad("restore takes prompts of at least one token")
+        stream = self.torch.cuda.current_stream(self.device)
+        k, v = codec.decode(blob, blob_bytes, token_ids, seq_offsets, stream=stream)
+        seqs = [self.add() for _ in counts]
+        try:
+            batch = self.extend(seqs, counts)
+        except DckvError:
+            for s in seqs:
+                self.drop(s)
+            raise
+        self.append(batch, k, v, rotate=False)
+        return seqs
+
+    def rows(self, seqs, counts=None):
+        """The first counts[i] (default: all) tokens of each sequence as pre-RoPE rows, and their
+        offsets: the arguments of Codec.encode."""
+        counts = [self._len[s] for s in seqs] if counts is None else [int(c) for c in counts]
+        n = sum(counts)
+        rows = self.torch.empty((n, 2 * self.pool.n_layers * self.pool.n_kv_heads * self.pool.head_dim),
+                                dtype=self.k.dtype, device=self.device)
+        dckv_cache_rows(self.pool, self._batch(seqs, counts), rows, self.status, rope=self.rope)
+        return rows, np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+
+    def store(self, codec, seqs, token_ids, counts=None):
+        """Encodes the sequences' first tokens with a codec: (blob, seq_offsets); codec.blob_size
+        and codec.status as after Codec.encode."""
+        rows, offsets = self.rows(seqs, counts)
+        stream = self.torch.cuda.current_stream(self.device)
+        return codec.encode(rows, token_ids, offsets, stream=stream), offsets

@@ -2179,3 +2179,7 @@ extern "C" int dckv_decode_static(const dckv_codec *c, const void *blob, size_t 
 
 // closed-form fit of the conditional models (calibration; not on the encode/decode path)
 #include "dckv_fit.cuh"
+
+// rotary positions, the paged KV cache and attention over it
+#include "dckv_cache.cuh"
+#include "dckv_attention.cuh"

@@ -1,0 +1,536 @@
+// dckv_cache.cuh -- rotary positions and the paged KV cache (include/dckv_cache.h): rotation of
+// strided tensors, the append of new keys and values to the pages, and the read-back of pages
+// as codec rows.  Included by dckv.cu (error text, device scope, launch count).
+//
+// All three move each element once and do 3 flops on it at most, so HBM bounds them on long
+// inputs and the launch and a chain of dependent loads bound them on short ones.  One block
+// takes one token: its threads compute the token's (cos, sin) pairs once, into shared memory,
+// and every head (and layer) of the token reads them from there -- the fp64 reduction and
+// sincosf cost about as much as the whole copy if each head repeats them.  Elements move as
+// 16-byte vectors: a "chunk" is two vectors, the two halves of V pairs (half layout) or V whole
+// pairs (interleaved layout).
+#pragma once
+#include "../../include/dckv_cache.h"
+#include "dckv_epilogues.cuh"
+
+namespace dckv {
+
+constexpr int CACHE_THREADS = 128;  // DCKV_ROPE_MAX_PAIRS: one pair per thread
+static_assert(CACHE_THREADS >= DCKV_ROPE_MAX_PAIRS, "one (cos, sin) pair per thread");
+
+// A rotation as the kernels take it (by value): mc and ms scale cos and sin (the magnitude, and
+// for the transpose the sign of sin).
+struct RopeDev {
+  int r = 0;  // rotary_dim; 0: copy
+  int interleaved = 0;
+  float mc = 1.f, ms = 1.f;
+  double freq[DCKV_ROPE_MAX_PAIRS] = {};
+};
+
+struct PoolDev {
+  char *k, *v;
+  int n_layers, heads, dim, page_size;
+  int64_t n_pages;
+  int64_t kl, kp, kr, kh, vl, vp, vr, vh;  // element strides: layer, page, row, head
+};
+
+struct BatchDev {
+  int batch, max_new, max_pages;
+  int64_t n;  // rows of the call's token tensors
+  const int32_t *offsets, *kv_lens, *page_table;
+  int64_t table_stride;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+
+// V consecutive elements: 16 bytes, or one element (odd sizes and alignments).
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Vec {
+  T e[V];
+};
+
+// Where chunk c of a rotated vector lies: its two V-element halves at off0 and off1 (off1 < 0:
+// absent, the odd last element of a scalar copy).  The first r / (2 V) chunks are pairs, the
+// rest copies.
+template <int V>
+__device__ __forceinline__ bool chunk_at(int c, int dim, const RopeDev &rope, int &off0, int &off1) {
+  const int pair_chunks = rope.r / (2 * V);
+  if (c < pair_chunks) {
+    off0 = rope.interleaved ? 2 * c * V : c * V;
+    off1 = rope.interleaved ? off0 + V : rope.r / 2 + c * V;
+    return true;
+  }
+  off0 = rope.r + 2 * (c - pair_chunks) * V;
+  off1 = off0 + V < dim ? off0 + V : -1;
+  return false;
+}
+
+// Rotates the V pairs of chunk c in place, fp32, one rounding.  cs: the token's pairs.
+template <typename T, int V>
+__device__ __forceinline__ void rotate_chunk(Vec<T, V> &x0, Vec<T, V> &x1, const float2 *cs, int c, bool interleaved) {
+  float u[2 * V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    u[j] = to_f(x0.e[j]);
+    u[V + j] = to_f(x1.e[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float2 w = cs[c * V + j];
+    const float a = interleaved ? u[2 * j] : u[j], b = interleaved ? u[2 * j + 1] : u[V + j];
+    const float a2 = a * w.x - b * w.y, b2 = b * w.x + a * w.y;
+    if (interleaved) {
+      u[2 * j] = a2;
+      u[2 * j + 1] = b2;
+    } else {
+      u[j] = a2;
+      u[V + j] = b2;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    x0.e[j] = from_f<T>(u[j]);
+    x1.e[j] = from_f<T>(u[V + j]);
+  }
+}
+
+// One pair's (cos, sin) of the token at position pos, the same angle reduction as the decoder's
+// RoPE, scaled as the mode asks.
+__device__ __forceinline__ float2 rope_pair(const RopeDev &rope, int pos, int i) {
+  float c, s;
+  rope_cs(pos, i, rope.freq, c, s);
+  return make_float2(c * rope.mc, s * rope.ms);
+}
+
+// ------------------------------------------------------------------ rotation of a tensor
+struct RopeArgs {
+  const char *x;
+  char *out;
+  int64_t xt, xh, ot, oh;  // element strides: token, head
+  int64_t n;
+  int heads, dim;
+  int in_place;            // dims past rotary_dim already stand in out
+  const int32_t *positions;
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(CACHE_THREADS) k_rope(const __grid_constant__ RopeDev rope, const RopeArgs a) {
+  __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
+  const int chunks = a.in_place ? rope.r / (2 * V) : rope.r / (2 * V) + (a.dim - rope.r + 2 * V - 1) / (2 * V);
+  for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x) {
+    if (threadIdx.x < rope.r / 2) cs[threadIdx.x] = rope_pair(rope, __ldg(a.positions + t), threadIdx.x);
+    __syncthreads();
+    const T *x = reinterpret_cast<const T *>(a.x) + t * a.xt;
+    T *out = reinterpret_cast<T *>(a.out) + t * a.ot;
+    for (int it = threadIdx.x; it < a.heads * chunks; it += CACHE_THREADS) {
+      const int h = it / chunks, c = it - h * chunks;
+      int o0, o1;
+      const bool turn = chunk_at<V>(c, a.dim, rope, o0, o1);
+      Vec<T, V> x0 = *reinterpret_cast<const Vec<T, V> *>(x + h * a.xh + o0), x1 = x0;
+      if (o1 >= 0) x1 = *reinterpret_cast<const Vec<T, V> *>(x + h * a.xh + o1);
+      if (turn) rotate_chunk<T, V>(x0, x1, cs, c, rope.interleaved);
+      *reinterpret_cast<Vec<T, V> *>(out + h * a.oh + o0) = x0;
+      if (o1 >= 0) *reinterpret_cast<Vec<T, V> *>(out + h * a.oh + o1) = x1;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ tokens, sequences, slots
+// Sequence of token t (all threads of the block call it; -1: none).  A batch of up to four
+// offsets per thread is scanned with one load latency, a larger one bisected.
+__device__ __forceinline__ int find_sequence(const BatchDev &bt, int64_t t, int *shared_b) {
+  if (bt.batch <= 4 * CACHE_THREADS) {
+    if (threadIdx.x == 0) *shared_b = -1;
+    __syncthreads();
+    for (int b = threadIdx.x; b < bt.batch; b += CACHE_THREADS)
+      if (t >= __ldg(bt.offsets + b) && t < __ldg(bt.offsets + b + 1)) *shared_b = b;
+    __syncthreads();
+    return *shared_b;
+  }
+  int lo = 0, hi = bt.batch;  // last b with offsets[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(bt.offsets + mid) <= t) lo = mid; else hi = mid;
+  }
+  return t >= __ldg(bt.offsets + lo) && t < __ldg(bt.offsets + lo + 1) ? lo : -1;
+}
+
+// Page of slot j of sequence b, or -1 where the table or the pool ends before it.
+__device__ __forceinline__ int64_t slot_page(const PoolDev &p, const BatchDev &bt, int b, int64_t j, int &row) {
+  const int64_t pi = j / p.page_size;
+  row = (int)(j - pi * p.page_size);
+  if (j < 0 || pi >= bt.max_pages) return -1;
+  const int page = __ldg(bt.page_table + b * bt.table_stride + pi);
+  return page >= 0 && page < p.n_pages ? page : -1;
+}
+
+struct AppendDev {
+  const char *k, *v, *q;
+  char *q_out;
+  int64_t kl, kt, kh, vl, vt, vh, qt, qh, ot, oh;
+  int n_q_heads;
+  const int32_t *positions;
+  int32_t *status;
+};
+
+// One token: its keys of every layer and head (rotated), its values (copied) and its queries
+// (rotated).
+template <typename T, int V>
+__global__ void __launch_bounds__(CACHE_THREADS)
+    k_append(const __grid_constant__ RopeDev rope, const PoolDev p, const BatchDev bt, const AppendDev a) {
+  __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
+  __shared__ int shared_b;
+  const int64_t t = blockIdx.x;
+  const int b = find_sequence(bt, t, &shared_b);
+  if (b < 0) return;
+  const int64_t first = __ldg(bt.offsets + b), n = __ldg(bt.offsets + b + 1) - first;
+  const int64_t j = (int64_t)__ldg(bt.kv_lens + b) - n + (t - first);
+  int row;
+  const int64_t page = slot_page(p, bt, b, j, row);
+  if (page < 0 || n > bt.max_new || first < 0 || first + n > bt.n) {
+    if (threadIdx.x == 0) atomicExch(a.status, DCKV_ERANGE);
+    return;
+  }
+  if (threadIdx.x < rope.r / 2)
+    cs[threadIdx.x] = rope_pair(rope, a.positions ? __ldg(a.positions + t) : (int)j, threadIdx.x);
+  __syncthreads();
+  const int chunks = p.dim / (2 * V);  // head_dim is a multiple of 2 V for both V
+  const int kv = p.n_layers * p.heads;
+  for (int it = threadIdx.x; it < (2 * kv + a.n_q_heads) * chunks; it += CACHE_THREADS) {
+    const int vec = it / chunks, c = it - vec * chunks;
+    const T *src;
+    T *dst;
+    bool turn = rope.r > 0;
+    if (vec < 2 * kv) {
+      const bool is_v = vec >= kv;
+      const int lh = is_v ? vec - kv : vec, l = lh / p.heads, h = lh - l * p.heads;
+      src = is_v ? reinterpret_cast<const T *>(a.v) + l * a.vl + t * a.vt + h * a.vh
+                 : reinterpret_cast<const T *>(a.k) + l * a.kl + t * a.kt + h * a.kh;
+      dst = is_v ? reinterpret_cast<T *>(p.v) + l * p.vl + page * p.vp + row * p.vr + h * p.vh
+                 : reinterpret_cast<T *>(p.k) + l * p.kl + page * p.kp + row * p.kr + h * p.kh;
+      turn = turn && !is_v;
+    } else {
+      const int h = vec - 2 * kv;
+      src = reinterpret_cast<const T *>(a.q) + t * a.qt + h * a.qh;
+      dst = reinterpret_cast<T *>(a.q_out) + t * a.ot + h * a.oh;
+    }
+    int o0, o1;
+    const bool pairs = chunk_at<V>(c, p.dim, rope, o0, o1);
+    Vec<T, V> x0 = *reinterpret_cast<const Vec<T, V> *>(src + o0), x1 = *reinterpret_cast<const Vec<T, V> *>(src + o1);
+    if (turn && pairs) rotate_chunk<T, V>(x0, x1, cs, c, rope.interleaved);
+    *reinterpret_cast<Vec<T, V> *>(dst + o0) = x0;
+    *reinterpret_cast<Vec<T, V> *>(dst + o1) = x1;
+  }
+}
+
+// One slot of a prompt as a row [layer][K, V][head][dim], keys rotated back.
+template <typename T, int V>
+__global__ void __launch_bounds__(CACHE_THREADS)
+    k_rows(const __grid_constant__ RopeDev rope, const PoolDev p, const BatchDev bt, char *rows, int64_t row_stride,
+           const int32_t *positions, int32_t *status) {
+  __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
+  __shared__ int shared_b;
+  const int64_t t = blockIdx.x;
+  const int b = find_sequence(bt, t, &shared_b);
+  if (b < 0) return;
+  const int64_t first = __ldg(bt.offsets + b), j = t - first;
+  int row;
+  const int64_t page = slot_page(p, bt, b, j, row);
+  if (page < 0 || j >= __ldg(bt.kv_lens + b) || first < 0 || __ldg(bt.offsets + b + 1) > bt.n) {
+    if (threadIdx.x == 0) atomicExch(status, DCKV_ERANGE);
+    return;
+  }
+  if (threadIdx.x < rope.r / 2)
+    cs[threadIdx.x] = rope_pair(rope, positions ? __ldg(positions + t) : (int)j, threadIdx.x);
+  __syncthreads();
+  const int chunks = p.dim / (2 * V);
+  T *out = reinterpret_cast<T *>(rows) + t * row_stride;
+  for (int it = threadIdx.x; it < 2 * p.n_layers * p.heads * chunks; it += CACHE_THREADS) {
+    const int vec = it / chunks, c = it - vec * chunks;  // vec = (layer * 2 + v) * heads + head
+    const int lv = vec / p.heads, h = vec - lv * p.heads, l = lv >> 1;
+    const bool is_v = lv & 1;
+    const T *src = is_v ? reinterpret_cast<const T *>(p.v) + l * p.vl + page * p.vp + row * p.vr + h * p.vh
+                        : reinterpret_cast<const T *>(p.k) + l * p.kl + page * p.kp + row * p.kr + h * p.kh;
+    int o0, o1;
+    const bool pairs = chunk_at<V>(c, p.dim, rope, o0, o1);
+    Vec<T, V> x0 = *reinterpret_cast<const Vec<T, V> *>(src + o0), x1 = *reinterpret_cast<const Vec<T, V> *>(src + o1);
+    if (!is_v && pairs) rotate_chunk<T, V>(x0, x1, cs, c, rope.interleaved);
+    *reinterpret_cast<Vec<T, V> *>(out + (int64_t)vec * p.dim + o0) = x0;
+    *reinterpret_cast<Vec<T, V> *>(out + (int64_t)vec * p.dim + o1) = x1;
+  }
+}
+
+}  // namespace dckv
+
+// ============================================================================ host checks
+static int check_device(int device) {
+  if (device < 0 || device >= 64) return fail(DCKV_EINVAL, "device %d out of range", device);
+  return DCKV_OK;
+}
+
+static int check_spec(const dckv_rope_spec *s, int mode, RopeDev &d) {
+  if (s->rotary_dim < 2 || s->rotary_dim > 2 * DCKV_ROPE_MAX_PAIRS || s->rotary_dim % 2)
+    return fail(DCKV_EINVAL, "rotary_dim %d must be even, 2 .. %d", s->rotary_dim, 2 * DCKV_ROPE_MAX_PAIRS);
+  if (s->layout != DCKV_ROPE_HALF && s->layout != DCKV_ROPE_INTERLEAVED)
+    return fail(DCKV_EINVAL, "unknown rotary layout %d", s->layout);
+  if (mode != DCKV_ROPE_FORWARD && mode != DCKV_ROPE_GRADIENT && mode != DCKV_ROPE_INVERSE)
+    return fail(DCKV_EINVAL, "unknown rotary mode %d", mode);
+  if (!std::isfinite(s->magnitude) || !(s->magnitude > 0.0))
+    return fail(DCKV_EINVAL, "rotary magnitude must be finite and positive");
+  for (int i = 0; i < s->rotary_dim / 2; ++i) {
+    if (!std::isfinite(s->freq[i])) return fail(DCKV_EINVAL, "rotary frequency %d is not finite", i);
+    d.freq[i] = s->freq[i];
+  }
+  d.r = s->rotary_dim;
+  d.interleaved = s->layout == DCKV_ROPE_INTERLEAVED;
+  d.mc = (float)(mode == DCKV_ROPE_INVERSE ? 1.0 / s->magnitude : s->magnitude);
+  d.ms = mode == DCKV_ROPE_FORWARD ? d.mc : -d.mc;
+  return DCKV_OK;
+}
+
+// A stride counts only where its dimension has more than one entry.
+static bool bad_stride(int64_t stride, int64_t extent, int64_t multiple) {
+  return extent > 1 && (stride <= 0 || stride % multiple || stride >= ((int64_t)1 << 38));
+}
+
+static int check_pool(const dckv_kv_pool *p, PoolDev &d) {
+  if (!p) return fail(DCKV_EINVAL, "pool is NULL");
+  RET(check_device(p->device));
+  if (!p->k || !p->v) return fail(DCKV_EINVAL, "a pool pointer is NULL");
+  if (((uintptr_t)p->k & 15) || ((uintptr_t)p->v & 15)) return fail(DCKV_EINVAL, "pool must be 16-byte aligned");
+  if (p->dtype != DCKV_BF16 && p->dtype != DCKV_FP16) return fail(DCKV_EINVAL, "pool type must be bf16 or fp16");
+  if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256)
+    return fail(DCKV_EINVAL, "head_dim %d must be 64, 128 or 256", p->head_dim);
+  if (p->page_size < 16 || p->page_size > 65536 || p->page_size % 16)
+    return fail(DCKV_EINVAL, "page_size %d must be a multiple of 16, 16 .. 65536", p->page_size);
+  if (p->n_layers < 1 || p->n_layers > 65535 || p->n_kv_heads < 1 || p->n_kv_heads > 65535 ||
+      (int64_t)p->n_layers * p->n_kv_heads > 65535)
+    return fail(DCKV_EINVAL, "pool layers or heads out of range");
+  if (p->n_pages < 1 || p->n_pages > 0x7fffffffll) return fail(DCKV_EINVAL, "n_pages out of range");
+  if (bad_stride(p->k_layer_stride, p->n_layers, 8) || bad_stride(p->v_layer_stride, p->n_layers, 8) ||
+      bad_stride(p->k_page_stride, p->n_pages, 8) || bad_stride(p->v_page_stride, p->n_pages, 8) ||
+      bad_stride(p->k_row_stride, p->page_size, 8) || bad_stride(p->v_row_stride, p->page_size, 8) ||
+      bad_stride(p->k_head_stride, p->n_kv_heads, 8) || bad_stride(p->v_head_stride, p->n_kv_heads, 8))
+    return fail(DCKV_EINVAL, "pool strides must be positive multiples of 8 elements");
+  d = PoolDev{(char *)p->k,       (char *)p->v,       p->n_layers,     p->n_kv_heads,   p->head_dim,
+              p->page_size,       p->n_pages,         p->k_layer_stride, p->k_page_stride, p->k_row_stride,
+              p->k_head_stride,   p->v_layer_stride,  p->v_page_stride, p->v_row_stride,  p->v_head_stride};
+  return DCKV_OK;
+}
+
+static int check_batch(const dckv_cache_batch *b, int64_t n_tokens, BatchDev &d) {
+  if (!b) return fail(DCKV_EINVAL, "batch is NULL");
+  if (!b->offsets || !b->kv_lens || !b->page_table) return fail(DCKV_EINVAL, "a batch pointer is NULL");
+  if (((uintptr_t)b->offsets & 3) || ((uintptr_t)b->kv_lens & 3) || ((uintptr_t)b->page_table & 3))
+    return fail(DCKV_EINVAL, "batch arrays must be 4-byte aligned");
+  if (b->batch < 1 || b->batch > DCKV_MAX_PROMPTS) return fail(DCKV_EINVAL, "batch %d out of range", b->batch);
+  if (b->max_new < 1 || b->max_new > (1 << 30)) return fail(DCKV_EINVAL, "max_new %d out of range", b->max_new);
+  if (b->max_pages < 1) return fail(DCKV_EINVAL, "max_pages must be positive");
+  if (b->reserved != 0) return fail(DCKV_EINVAL, "reserved fields must be 0");
+  if (b->batch > 1 && b->table_stride < b->max_pages)
+    return fail(DCKV_EINVAL, "table_stride is smaller than max_pages");
+  d = BatchDev{b->batch, b->max_new, b->max_pages, n_tokens, b->offsets, b->kv_lens, b->page_table, b->table_stride};
+  return DCKV_OK;
+}
+
+// Bytes spanned by [n][heads][dim] with the given element strides (up to 2^38 each: 128 bits).
+static unsigned __int128 span_bytes(int64_t n, int64_t ts, int64_t heads, int64_t hs, int64_t dim, int size) {
+  return ((unsigned __int128)(n - 1) * ts + (unsigned __int128)(heads - 1) * hs + dim) * size;
+}
+
+static bool overlaps(const void *a, unsigned __int128 an, const void *b, unsigned __int128 bn) {
+  return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
+
+// Whole vectors of v elements: pair chunks, copy chunks and every address.
+static bool rope_vectors(int r, int dim, int v) { return r % (2 * v) == 0 && (dim - r) % (2 * v) == 0; }
+
+extern "C" int dckv_rope_init(dckv_rope_spec *out, int rotary_dim, int layout, double base, int scaling, double factor,
+                              double original_len, double low, double high, double magnitude) {
+  if (!out) return fail(DCKV_EINVAL, "out is NULL");
+  if (!std::isfinite(base) || !(base > 1.0)) return fail(DCKV_EINVAL, "rotary base must be finite and above 1");
+  if (scaling < DCKV_ROPE_NONE || scaling > DCKV_ROPE_PARTS) return fail(DCKV_EINVAL, "unknown rotary scaling %d", scaling);
+  if (scaling != DCKV_ROPE_NONE && (!std::isfinite(factor) || !(factor > 0.0)))
+    return fail(DCKV_EINVAL, "rotary factor must be finite and positive");
+  if (scaling == DCKV_ROPE_NTK && rotary_dim <= 2) return fail(DCKV_EINVAL, "this scaling needs rotary_dim above 2");
+  if (scaling == DCKV_ROPE_PARTS && (!(original_len > 0.0) || !std::isfinite(original_len) || !std::isfinite(low) ||
+                                     !std::isfinite(high) || !(high > low)))
+    return fail(DCKV_EINVAL, "this scaling needs original_len > 0 and high > low");
+  dckv_rope_spec s = {};
+  s.rotary_dim = rotary_dim;
+  s.layout = layout;
+  s.magnitude = magnitude;
+  RopeDev d;
+  RET(check_spec(&s, DCKV_ROPE_FORWARD, d));  // sizes, layout and magnitude (frequencies are still 0)
+  const double b = scaling == DCKV_ROPE_NTK ? base * std::pow(factor, (double)rotary_dim / (rotary_dim - 2)) : base;
+  if (!std::isfinite(b) || !(b > 0.0)) return fail(DCKV_EINVAL, "the scaled rotary base is out of range");
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(b, -2.0 * i / rotary_dim);
+    if (scaling == DCKV_ROPE_LINEAR) f /= factor;
+    if (scaling == DCKV_ROPE_PARTS) {
+      const double turns = original_len * f / 6.283185307179586;
+      const double w = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+      f *= w + (1.0 - w) / factor;
+    }
+    s.freq[i] = f;
+  }
+  *out = s;
+  return DCKV_OK;
+}
+
+extern "C" int dckv_rope(const dckv_rope_spec *spec, int mode, int device, int dtype, const void *x, int64_t x_token_stride,
+                         int64_t x_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride,
+                         int64_t n_tokens, int n_heads, int head_dim, const int32_t *positions, void *stream) {
+  if (!spec || !x || !out || !positions) return fail(DCKV_EINVAL, "a pointer argument is NULL");
+  RET(check_device(device));
+  RopeDev rope;
+  RET(check_spec(spec, mode, rope));
+  if (dtype != DCKV_BF16 && dtype != DCKV_FP16 && dtype != DCKV_FP32) return fail(DCKV_EINVAL, "unknown type %d", dtype);
+  const int size = dtype == DCKV_FP32 ? 4 : 2;
+  if (((uintptr_t)x & (size - 1)) || ((uintptr_t)out & (size - 1)) || ((uintptr_t)positions & 3))
+    return fail(DCKV_EINVAL, "a tensor is not aligned to its elements");
+  if (n_tokens < 0 || n_tokens > 0x7fffffffll || n_heads < 1 || n_heads > 65535)
+    return fail(DCKV_EINVAL, "n_tokens or n_heads out of range");
+  if (head_dim < rope.r || head_dim > 65536) return fail(DCKV_EINVAL, "head_dim %d out of range", head_dim);
+  if (bad_stride(x_token_stride, n_tokens, 1) || bad_stride(x_head_stride, n_heads, 1) ||
+      bad_stride(out_token_stride, n_tokens, 1) || bad_stride(out_head_stride, n_heads, 1))
+    return fail(DCKV_EINVAL, "strides must be positive");
+  if (n_tokens == 0) return DCKV_OK;
+  const bool same = x == out && (n_tokens == 1 || x_token_stride == out_token_stride) &&
+                    (n_heads == 1 || x_head_stride == out_head_stride);
+  if (n_tokens == 1) x_token_stride = out_token_stride = 0;
+  if (n_heads == 1) x_head_stride = out_head_stride = 0;
+  if (!same && overlaps(x, span_bytes(n_tokens, x_token_stride, n_heads, x_head_stride, head_dim, size), out,
+                        span_bytes(n_tokens, out_token_stride, n_heads, out_head_stride, head_dim, size)))
+    return fail(DCKV_EINVAL, "out overlaps x without being x");
+  const int v = 16 / size;
+  const bool vec = rope_vectors(rope.r, head_dim, v) && !(((uintptr_t)x | (uintptr_t)out) & 15) &&
+                   !((x_token_stride | x_head_stride | out_token_stride | out_head_stride) % v);
+  const RopeArgs a{(const char *)x, (char *)out, x_token_stride, x_head_stride, out_token_stride, out_head_stride,
+                   n_tokens, n_heads, head_dim, same ? 1 : 0, positions};
+  cudaStream_t st = (cudaStream_t)stream;
+  DEVICE_SCOPE(device);
+  const unsigned grid = (unsigned)n_tokens;
+  if (dtype == DCKV_FP32) {
+    if (vec) k_rope<float, 4><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+    else k_rope<float, 1><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+  } else if (dtype == DCKV_FP16) {
+    if (vec) k_rope<__half, 8><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+    else k_rope<__half, 1><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+  } else {
+    if (vec) k_rope<__nv_bfloat16, 8><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+    else k_rope<__nv_bfloat16, 1><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+  }
+  ++g_launches;
+  CK(cudaGetLastError());
+  return DCKV_OK;
+}
+
+extern "C" int dckv_cache_append(const dckv_kv_pool *pool, const dckv_cache_batch *batch, const dckv_rope_spec *rope,
+                                 const dckv_append_args *args, int32_t *status, void *stream) {
+  PoolDev p;
+  BatchDev b;
+  RopeDev r;
+  RET(check_pool(pool, p));
+  RET(check_batch(batch, args ? args->n_tokens : 0, b));
+  if (!args || !args->k || !args->v || !status) return fail(DCKV_EINVAL, "a pointer argument is NULL");
+  if (((uintptr_t)args->k & 15) || ((uintptr_t)args->v & 15) || ((uintptr_t)status & 3) ||
+      ((uintptr_t)args->positions & 3))
+    return fail(DCKV_EINVAL, "k and v must be 16-byte, status and positions 4-byte aligned");
+  if (rope) RET(check_spec(rope, DCKV_ROPE_FORWARD, r));
+  if (r.r > p.dim) return fail(DCKV_EINVAL, "rotary_dim is larger than head_dim");
+  const int64_t n = args->n_tokens;
+  if (n < 0 || n > 0x7fffffffll) return fail(DCKV_EINVAL, "n_tokens out of range");
+  if (args->reserved != 0) return fail(DCKV_EINVAL, "reserved fields must be 0");
+  if (bad_stride(args->k_layer_stride, p.n_layers, 8) || bad_stride(args->k_token_stride, n, 8) ||
+      bad_stride(args->k_head_stride, p.heads, 8) || bad_stride(args->v_layer_stride, p.n_layers, 8) ||
+      bad_stride(args->v_token_stride, n, 8) || bad_stride(args->v_head_stride, p.heads, 8))
+    return fail(DCKV_EINVAL, "k and v strides must be positive multiples of 8 elements");
+  AppendDev a{(const char *)args->k, (const char *)args->v, nullptr, nullptr, args->k_layer_stride,
+              args->k_token_stride, args->k_head_stride, args->v_layer_stride, args->v_token_stride,
+              args->v_head_stride, args->q_token_stride, args->q_head_stride, args->q_out_token_stride,
+              args->q_out_head_stride, 0, args->positions, status};
+  if (args->q) {
+    const int hq = args->n_q_heads;
+    if (!rope) return fail(DCKV_EINVAL, "q needs a rotation");
+    if (!args->q_out) return fail(DCKV_EINVAL, "q_out is NULL");
+    if (((uintptr_t)args->q & 15) || ((uintptr_t)args->q_out & 15))
+      return fail(DCKV_EINVAL, "q and q_out must be 16-byte aligned");
+    if (hq < 1 || hq > 65535) return fail(DCKV_EINVAL, "n_q_heads out of range");
+    if (bad_stride(a.qt, n, 8) || bad_stride(a.qh, hq, 8) || bad_stride(a.ot, n, 8) || bad_stride(a.oh, hq, 8))
+      return fail(DCKV_EINVAL, "q and q_out strides must be positive multiples of 8 elements");
+    if (n <= 1) a.qt = a.ot = 0;
+    if (hq == 1) a.qh = a.oh = 0;
+    const bool same = args->q == args->q_out && a.qt == a.ot && a.qh == a.oh;
+    if (n > 0 && !same && overlaps(args->q, span_bytes(n, a.qt, hq, a.qh, p.dim, 2), args->q_out,
+                                   span_bytes(n, a.ot, hq, a.oh, p.dim, 2)))
+      return fail(DCKV_EINVAL, "q_out overlaps q without being q");
+    a.q = (const char *)args->q;
+    a.q_out = (char *)args->q_out;
+    a.n_q_heads = hq;
+  }
+  if (n == 0) return DCKV_OK;
+  cudaStream_t st = (cudaStream_t)stream;
+  DEVICE_SCOPE(pool->device);
+  const bool vec = rope_vectors(r.r, p.dim, 8);
+  // 16-bit types: the copies do not look at them, the rotation does
+  if (pool->dtype == DCKV_BF16) {
+    if (vec) k_append<__nv_bfloat16, 8><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
+    else k_append<__nv_bfloat16, 1><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
+  } else {
+    if (vec) k_append<__half, 8><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
+    else k_append<__half, 1><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
+  }
+  ++g_launches;
+  CK(cudaGetLastError());
+  return DCKV_OK;
+}
+
+extern "C" int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch *batch, const dckv_rope_spec *rope,
+                               void *rows, int64_t row_stride, int64_t n_tokens, const int32_t *positions,
+                               int32_t *status, void *stream) {
+  PoolDev p;
+  BatchDev b;
+  RopeDev r;
+  RET(check_pool(pool, p));
+  RET(check_batch(batch, n_tokens, b));
+  if (!rows || !status) return fail(DCKV_EINVAL, "a pointer argument is NULL");
+  if (((uintptr_t)rows & 15) || ((uintptr_t)status & 3) || ((uintptr_t)positions & 3))
+    return fail(DCKV_EINVAL, "rows must be 16-byte, status and positions 4-byte aligned");
+  if (rope) RET(check_spec(rope, DCKV_ROPE_INVERSE, r));
+  if (r.r > p.dim) return fail(DCKV_EINVAL, "rotary_dim is larger than head_dim");
+  if (n_tokens < 0 || n_tokens > 0x7fffffffll) return fail(DCKV_EINVAL, "n_tokens out of range");
+  if (n_tokens > 1 && (row_stride % 8 || row_stride < (int64_t)2 * p.n_layers * p.heads * p.dim ||
+                       row_stride >= ((int64_t)1 << 38)))
+    return fail(DCKV_EINVAL, "row_stride must be a multiple of 8 and hold a row");
+  if (n_tokens == 0) return DCKV_OK;
+  cudaStream_t st = (cudaStream_t)stream;
+  DEVICE_SCOPE(pool->device);
+  const bool vec = rope_vectors(r.r, p.dim, 8);
+  if (pool->dtype == DCKV_BF16) {
+    if (vec) k_rows<__nv_bfloat16, 8><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
+    else k_rows<__nv_bfloat16, 1><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
+  } else {
+    if (vec) k_rows<__half, 8><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
+    else k_rows<__half, 1><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
+  }
+  ++g_launches;
+  CK(cudaGetLastError());
+  return DCKV_OK;
+}
