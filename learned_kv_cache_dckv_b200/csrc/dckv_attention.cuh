@@ -1,84 +1,735 @@
 // dckv_attention.cuh -- attention of new tokens over the paged cache (include/dckv_cache.h).
 // Included by dckv.cu after dckv_cache.cuh.
+//
+// Mathematics.  With x_j = log2(e) scale q . k_j, a pass over any subset of a row's slots keeps
+// m = max x_j, l = sum 2^(x_j - m) and O = sum 2^(x_j - m) v_j; two subsets join by scaling the
+// one with the smaller m by 2^(m1 - m2).  So slots can be split anywhere: over warps, blocks and
+// tiles, and the parts added at the end.
+//
+// Rows.  The g query heads of a KV head read the same keys, so a row tile packs (token, head of
+// the group) pairs: packed row i of a sequence is token i / g, head i % g.
+//
+// Work.  A unit is (KV head, sequence, row tile); its tiles are the key tiles that its last row
+// sees.  The units' tiles stand in one line, head after head, and every block takes an equal,
+// contiguous piece of that line, whatever the sequences' lengths: a piece that begins or ends
+// inside a unit leaves its part (m, l, O) in the workspace, and a second kernel joins the parts.
+// A block finds its piece by itself from the lengths on the device, so the host needs none.
 #pragma once
 #include "dckv_cache.cuh"
 
 namespace dckv {
+
+constexpr int ATTN_MAX_WORKERS = 160;  // workspace slots; at most one worker per SM
 
 struct AttnDev {
   const char *q;
   char *out;
   float *lse;
   int64_t qt, qh, ot, oh;
-  int64_t n;
-  int heads, group, layer, causal;
-  float scale;
+  int heads, group, causal;
+  float scale_log2;
   int32_t *status;
+  float *part_o;   // [2 workers][rows][dim]
+  float2 *part_ml; // [2 workers][rows] (m, l)
+  int4 *desc;      // [workers] {unit, KV head, last worker, rows}: a unit begins here and is split
+  int workers;
 };
 
-// One block per token, one warp per query head in turn; lane l holds dims l, l + 32, ...
-// (the first, plain form: every row reads its keys and values by itself).
-template <typename T, int D>
-__global__ void __launch_bounds__(CACHE_THREADS) k_attend(const PoolDev p, const BatchDev bt, const AttnDev a) {
-  __shared__ int shared_b;
-  const int64_t t = blockIdx.x;
-  const int b = find_sequence(bt, t, &shared_b);
-  if (b < 0) return;
-  const int64_t first = __ldg(bt.offsets + b), n = __ldg(bt.offsets + b + 1) - first;
-  const int64_t len = __ldg(bt.kv_lens + b);
-  if (n > bt.max_new || first < 0 || first + n > bt.n || len < 0 || len > (int64_t)bt.max_pages * p.page_size) {
-    if (threadIdx.x == 0) atomicExch(a.status, DCKV_ERANGE);
-    return;
-  }
-  const int64_t seen = a.causal ? len - n + (t - first) + 1 : len;
-  const int lane = threadIdx.x & 31;
-  constexpr int E = D / 32;
-  for (int h = threadIdx.x >> 5; h < a.heads; h += CACHE_THREADS / 32) {
-    const T *q = reinterpret_cast<const T *>(a.q) + t * a.qt + h * a.qh;
-    const T *k = reinterpret_cast<const T *>(p.k) + a.layer * p.kl + (h / a.group) * p.kh;
-    const T *v = reinterpret_cast<const T *>(p.v) + a.layer * p.vl + (h / a.group) * p.vh;
-    float x[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      x[e] = to_f(q[lane + 32 * e]) * a.scale;
-      o[e] = 0.f;
+// What the kernels know of one sequence.
+struct SeqView {
+  int64_t first;  // first token
+  int n, len;     // new tokens, slots in use
+};
+
+__device__ __forceinline__ bool load_seq(const BatchDev &bt, int64_t max_slots, int b, SeqView &s) {
+  s.first = __ldg(bt.offsets + b);
+  const int64_t n = (int64_t)__ldg(bt.offsets + b + 1) - s.first;
+  s.len = __ldg(bt.kv_lens + b);
+  s.n = (int)n;
+  const bool ok = s.first >= 0 && n >= 0 && n <= bt.max_new && s.first + n <= bt.n && s.len >= 0 && s.len <= max_slots;
+  if (!ok) s.n = s.len = 0;
+  return ok;
+}
+
+// Slots that token t of the sequence sees.
+__device__ __forceinline__ int seen_slots(const SeqView &s, int t, int causal) {
+  return causal ? max(0, s.len - s.n + t + 1) : s.len;
+}
+
+// Slots that row tile rt sees (its last row's), -1 where it has no rows.
+__device__ __forceinline__ int tile_seen(const SeqView &s, int rt, int rows, int group, int causal) {
+  const int64_t n_rows = (int64_t)s.n * group, r0 = (int64_t)rt * rows;
+  if (r0 >= n_rows) return -1;
+  const int64_t last = min(n_rows, r0 + rows) - 1;
+  return seen_slots(s, (int)(last / group), causal);
+}
+
+// Key tiles of a unit; one that sees no slot still has one, to write its zeros.
+__device__ __forceinline__ int unit_tiles(int seen, int key_tile) {
+  return seen < 0 ? 0 : max(1, (int)(((int64_t)seen + key_tile - 1) / key_tile));
+}
+
+// A block's walk along the line of tiles: the current unit and the tiles [t0, t1) of it that
+// the block takes.
+struct AttnWalk {
+  int64_t left;   // tiles of the block's piece from t0 on
+  int head, unit; // unit = sequence * row tiles + row tile
+  int b, rt;
+  SeqView s;
+  int seen, tiles, t0, t1;
+};
+
+struct AttnShape {
+  int rows, key_tile, row_tiles, units, kv_heads;
+  int64_t max_slots;
+};
+
+// Fills the walk's unit fields from (head, unit); t0 is given.
+__device__ __forceinline__ void walk_load(AttnWalk &w, const BatchDev &bt, const AttnDev &a, const AttnShape &sh) {
+  w.b = w.unit / sh.row_tiles;
+  w.rt = w.unit - w.b * sh.row_tiles;
+  load_seq(bt, sh.max_slots, w.b, w.s);
+  w.seen = tile_seen(w.s, w.rt, sh.rows, a.group, a.causal);
+  w.tiles = unit_tiles(w.seen, sh.key_tile);
+  w.t1 = (int)min((int64_t)w.tiles, w.t0 + w.left);
+}
+
+// Steps to the next unit with tiles; false at the end of the piece.
+__device__ __forceinline__ bool walk_next(AttnWalk &w, const BatchDev &bt, const AttnDev &a, const AttnShape &sh) {
+  w.left -= w.t1 - w.t0;
+  if (w.left <= 0) return false;
+  w.t0 = 0;
+  do {
+    if (++w.unit == sh.units) {
+      w.unit = 0;
+      if (++w.head >= sh.kv_heads) return false;  // only if the lengths changed under the kernel
     }
-    for (int64_t j = 0; j < seen; ++j) {
-      int row;
-      const int64_t page = slot_page(p, bt, b, j, row);
-      if (page < 0) {
-        if (lane == 0) atomicExch(a.status, DCKV_ERANGE);
+    walk_load(w, bt, a, sh);
+  } while (w.tiles == 0);
+  return true;
+}
+
+struct AttnPlanSmem {
+  int64_t warp_sum[32];
+  int64_t total;
+  int unit, off;
+};
+
+struct AttnPlan {
+  int64_t total;  // tiles of one head's units
+  int64_t line;   // tiles of all heads
+  int workers;    // blocks that take a piece
+};
+
+// First tile of worker c's piece.
+__device__ __forceinline__ int64_t piece_start(const AttnPlan &pl, int c) { return (int64_t)c * pl.line / pl.workers; }
+
+// Worker whose piece holds tile p of the line.
+__device__ __forceinline__ int piece_of(const AttnPlan &pl, int64_t p) {
+  return (int)(((p + 1) * pl.workers + pl.line - 1) / pl.line) - 1;
+}
+
+// Counts every unit's tiles (each thread a run of units, then a block scan), and finds worker
+// c's start.  Called by all threads of the block; returns false where c has no piece.
+template <int THREADS>
+__device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, const AttnShape &sh, int min_tiles,
+                                          int c, AttnPlanSmem *sm, AttnPlan &pl, AttnWalk &w) {
+  constexpr int WARPS = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (sh.units + THREADS - 1) / THREADS;
+  const int u0 = min(sh.units, tid * per), u1 = min(sh.units, u0 + per);
+  int64_t mine = 0;
+  int b = -1;
+  SeqView s;
+  for (int u = u0; u < u1; ++u) {
+    const int bu = u / sh.row_tiles;
+    if (bu != b) {
+      b = bu;
+      const bool ok = load_seq(bt, sh.max_slots, b, s);
+      if (!ok && c == 0) atomicExch(a.status, DCKV_ERANGE);
+    }
+    mine += unit_tiles(tile_seen(s, u - b * sh.row_tiles, sh.rows, a.group, a.causal), sh.key_tile);
+  }
+  int64_t incl = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm->warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int i = 0; i < WARPS; ++i) {
+    const int64_t v = sm->warp_sum[i];
+    if (i < warp) before += v;
+    total += v;
+  }
+  pl.total = total;
+  pl.line = total * sh.kv_heads;
+  pl.workers = (int)max((int64_t)1, min((int64_t)a.workers, pl.line / min_tiles));
+  if (pl.line == 0 || c >= pl.workers) return false;
+  const int64_t start = piece_start(pl, c);
+  w.left = piece_start(pl, c + 1) - start;
+  w.head = (int)(start / total);
+  const int64_t pos = start - w.head * total;
+  int64_t at = before + incl - mine;
+  if (pos >= at && pos < at + mine) {  // the start lies in this thread's run: walk it
+    int u = u0;
+    for (; u < u1; ++u) {
+      const int bu = u / sh.row_tiles;
+      load_seq(bt, sh.max_slots, bu, s);
+      const int t = unit_tiles(tile_seen(s, u - bu * sh.row_tiles, sh.rows, a.group, a.causal), sh.key_tile);
+      if (pos < at + t) break;
+      at += t;
+    }
+    sm->unit = u;
+    sm->off = (int)(pos - at);
+  }
+  __syncthreads();
+  w.unit = sm->unit;
+  w.t0 = sm->off;
+  walk_load(w, bt, a, sh);
+  return true;
+}
+
+// ------------------------------------------------------------------ math helpers
+__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp and flush to zero (PTX ex2.approx.ftz)
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma_16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma_16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Where a unit's row r goes: token and query head; false past its last row.
+__device__ __forceinline__ bool unit_row(const AttnWalk &w, const AttnDev &a, int rows, int r, int64_t &tok, int &head,
+                                         int &seen) {
+  const int64_t i = (int64_t)w.rt * rows + r;
+  if (i >= (int64_t)w.s.n * a.group) return false;
+  const int t = (int)(i / a.group);
+  tok = w.s.first + t;
+  head = w.head * a.group + (int)(i - (int64_t)t * a.group);
+  seen = seen_slots(w.s, t, a.causal);
+  return true;
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T *dst, float4 v) {
+  uint2 p = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+  *reinterpret_cast<uint2 *>(dst) = p;
+}
+
+// ------------------------------------------------------------------ few rows: one warp, 16 keys
+// Rows 8 NT at most (single tokens of up to 16 query heads per KV head).  Every K and V byte is
+// used for 8 or 16 rows only, so HBM bounds it; the kernel's shape keeps as many loads in flight
+// as shared memory holds and no barrier in the loop.  Each of four warps runs its own ring of
+// stages (a slice of 16 keys: K and V, fetched by TMA with the 128-byte swizzle) and its own
+// (m, l, O), and the four are joined in shared memory at a unit's end.  mma.sync with the keys
+// as the M dimension: S^T = K Q^T and O^T = V^T P^T, so that 8 rows fill the N dimension that
+// would be padded to 16 (or 128) as M; P^T goes from accumulators to the second product's
+// operand through movmatrix.
+constexpr int DEC_ATTN_WARPS = 4;
+constexpr int DEC_ATTN_THREADS = 32 * DEC_ATTN_WARPS;
+constexpr int DEC_SLICE = 16;
+constexpr int DEC_KEY_TILE = DEC_SLICE * DEC_ATTN_WARPS;
+
+template <int D, int NT>
+struct DecodeAttn {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int SLICE_BYTES = DEC_SLICE * D * 2;
+  static constexpr int STAGE_BYTES = 2 * SLICE_BYTES;  // K, V
+  static constexpr int O_LD = D + 4;                   // floats per row of the join buffer (conflict-free)
+  static constexpr int JOIN_BYTES = DEC_ATTN_WARPS * ROWS * (O_LD * 4 + 8);
+  static constexpr int FIT = (232448 - 2048 - JOIN_BYTES) / (DEC_ATTN_WARPS * STAGE_BYTES);
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM = 1024 + DEC_ATTN_WARPS * STAGES * STAGE_BYTES + JOIN_BYTES;
+  static_assert(STAGES >= 2 && SMEM <= 232448 - 1024, "shared memory");
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
+    k_attend_few(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PoolDev p,
+                 const BatchDev bt, const AttnDev a, const AttnShape sh) {
+  using C = DecodeAttn<D, NT>;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  __shared__ AttnPlanSmem plan_sm;
+  __shared__ uint64_t full[DEC_ATTN_WARPS][C::STAGES][2];
+  __shared__ int abort_sm;
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t *ring = base + warp * C::STAGES * C::STAGE_BYTES;
+  float *join_o = reinterpret_cast<float *>(base + DEC_ATTN_WARPS * C::STAGES * C::STAGE_BYTES);
+  float2 *join_ml = reinterpret_cast<float2 *>(join_o + DEC_ATTN_WARPS * C::ROWS * C::O_LD);
+  volatile int *abort_flag = &abort_sm;
+
+  if (lane == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[warp][s][0], 1);
+      mbar_init(&full[warp][s][1], 1);
+    }
+    if (warp == 0) {
+      abort_sm = 0;
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
+    fence_mbar_init();
+  }
+  AttnPlan pl;
+  AttnWalk w;
+  const int c = blockIdx.x;
+  const bool any = attn_plan<DEC_ATTN_THREADS>(bt, a, sh, 1, c, &plan_sm, pl, w);
+  if (threadIdx.x == 0) a.desc[c] = make_int4(-1, 0, 0, 0);
+  if (!any) return;
+  __syncwarp();
+
+  // the producer's walk runs ahead of the consumer's: same slices, STAGES of them in flight
+  AttnWalk pw = w;
+  int pt = pw.t0;           // next tile of the producer
+  bool more = true;
+  uint32_t issued = 0, used = 0;
+  auto slice_key = [&](int t) { return t * DEC_KEY_TILE + warp * DEC_SLICE; };
+  bool ok = true;
+  auto produce = [&]() {  // issues the next slice of this warp, if there is one
+    while (more && ok) {
+      if (pt >= pw.t1) {
+        more = walk_next(pw, bt, a, sh);
+        pt = pw.t0;
         continue;
       }
-      float s = 0.f;
+      const int key = slice_key(pt++);
+      if (key >= pw.seen) continue;
+      if (lane == 0) {
+        const int pi = key / p.page_size;
+        int page = __ldg(bt.page_table + pw.b * bt.table_stride + pi);
+        if (page < 0 || page >= p.n_pages) {  // past the pool: the copy fills zeros
+          atomicExch(a.status, DCKV_ERANGE);
+          page = (int)p.n_pages;
+        }
+        const int row = key - pi * p.page_size;
+        const uint32_t s = issued % C::STAGES;
+        uint8_t *dst = ring + s * C::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[warp][s][0], C::SLICE_BYTES);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(x[e], to_f(k[page * p.kp + row * p.kr + lane + 32 * e]), s);
-      for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-      const float top = fmaxf(m, s), keep = __expf(m - top), w = __expf(s - top);
-      l = l * keep + w;
-      m = top;
+        for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * 2048, &tm_k, &full[warp][s][0], 64 * x, row, pw.head, page);
+        mbar_arrive_expect_tx(&full[warp][s][1], C::SLICE_BYTES);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        o[e] = fmaf(w, to_f(v[page * p.vp + row * p.vr + lane + 32 * e]), o[e] * keep);
+        for (int x = 0; x < D / 64; ++x)
+          tma_load_4d(dst + C::SLICE_BYTES + x * 2048, &tm_v, &full[warp][s][1], 64 * x, row, pw.head, page);
+      }
+      ++issued;
+      return;
     }
-    T *out = reinterpret_cast<T *>(a.out) + t * a.ot + h * a.oh;
+  };
+  for (int s = 0; s < C::STAGES; ++s) produce();
+
+  bool first_segment = true;
+  const int rq = lane >> 2, cq = lane & 3;  // fragment row and column pair
+  // ldmatrix source of this lane: matrix lane / 8, its row lane % 8
+  const int mi = lane >> 3, mr = lane & 7;
+  do {
+    // Q^T fragments: row (n) rq of each 8-row tile, dims 16 kk + 2 cq (+ 8)
+    uint32_t qf[NT][D / 16][2];
+    int seen[2 * NT];
+    int min_seen = 0x7fffffff;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[lane + 32 * e] = from_f<T>(l > 0.f ? o[e] / l : 0.f);
-    if (a.lse && lane == 0) a.lse[t * a.heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    for (int nt = 0; nt < NT; ++nt) {
+      int64_t tok;
+      int head, sn;
+      const bool valid = unit_row(w, a, C::ROWS, nt * 8 + rq, tok, head, sn);
+      const T *q = reinterpret_cast<const T *>(a.q) + (valid ? tok * a.qt + head * a.qh : 0);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[nt][kk][0] = valid ? __ldg(reinterpret_cast<const uint32_t *>(q + kk * 16 + 2 * cq)) : 0u;
+        qf[nt][kk][1] = valid ? __ldg(reinterpret_cast<const uint32_t *>(q + kk * 16 + 8 + 2 * cq)) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        seen[2 * nt + e] = 0x7fffffff;
+        if (unit_row(w, a, C::ROWS, nt * 8 + 2 * cq + e, tok, head, sn)) seen[2 * nt + e] = sn;
+        min_seen = min(min_seen, seen[2 * nt + e]);
+      }
+    }
+    min_seen = min(min_seen, w.seen);
+    min_seen = min(min_seen, __shfl_xor_sync(0xffffffffu, min_seen, 1));
+    min_seen = min(min_seen, __shfl_xor_sync(0xffffffffu, min_seen, 2));
+
+    float o[NT][D / 16][4], m[2 * NT], l[2 * NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2 * NT; ++e) {
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+    }
+
+    for (int t = w.t0; t < w.t1; ++t) {
+      const int key0 = slice_key(t);
+      if (key0 >= w.seen) break;  // this warp's slices of the unit end here
+      const uint32_t st = used % C::STAGES, parity = (used / C::STAGES) & 1u;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[warp][st][0], parity, abort_flag));
+      if (!ok) break;
+      const uint32_t ks = smem_u32(ring + st * C::STAGE_BYTES), vs = ks + C::SLICE_BYTES;
+      // S^T: four partial sums per row tile keep the products' latency apart
+      float s4[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s4[nt][i][e] = 0.f;
+      {
+        const int row = (mi & 1) * 8 + mr, hi = mi >> 1;  // matrices: keys 0-7, 8-15, then dims + 8
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int chunk = (kk & 3) * 2 + hi;
+          uint32_t kf[4];
+          ldmatrix_x4(kf, ks + (kk >> 2) * 2048 + row * 128 + ((chunk ^ mr) << 4));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816<T>(s4[nt][kk & 1], kf, qf[nt][kk][0], qf[nt][kk][1]);
+        }
+      }
+      const bool edge = key0 + DEC_SLICE > min_seen;
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = (s4[nt][0][e] + s4[nt][1][e]) * a.scale_log2;
+          if (edge && key0 + rq + (e >> 1) * 8 >= min(seen[2 * nt + (e & 1)], w.seen)) x[e] = -INFINITY;
+        }
+        float keep[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(x[e], x[e + 2]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          top = fmaxf(top, m[2 * nt + e]);
+          const float ref = top == -INFINITY ? 0.f : top;
+          keep[e] = exp2_fast(m[2 * nt + e] - ref);
+          m[2 * nt + e] = top;
+          x[e] = exp2_fast(x[e] - ref);
+          x[e + 2] = exp2_fast(x[e + 2] - ref);
+          l[2 * nt + e] = l[2 * nt + e] * keep[e] + x[e] + x[e + 2];
+        }
+        pf[nt][0] = transpose_8x8(pack2<T>(x[0], x[1]));
+        pf[nt][1] = transpose_8x8(pack2<T>(x[2], x[3]));
+        if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[nt][i][0] *= keep[0];
+            o[nt][i][1] *= keep[1];
+            o[nt][i][2] *= keep[0];
+            o[nt][i][3] *= keep[1];
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][st][1], parity, abort_flag));
+      if (!ok) break;
+      // rows of V behind the last slot in use may hold anything: their words become 0
+      const int live = w.s.len - key0;  // slots of the slice in use
+      const bool clean = live >= DEC_SLICE;
+      uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
+      if (!clean) {
+        const int k0 = 2 * cq;
+        keep_lo = (k0 < live ? 0xffffu : 0u) | (k0 + 1 < live ? 0xffff0000u : 0u);
+        keep_hi = (k0 + 8 < live ? 0xffffu : 0u) | (k0 + 9 < live ? 0xffff0000u : 0u);
+      }
+      {
+        const int row = (mi >> 1) * 8 + mr, hi = mi & 1;  // matrices: dims 0-7, 8-15, then keys + 8
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int chunk = (i & 3) * 2 + hi;
+          uint32_t vf[4];
+          ldmatrix_x4_trans(vf, vs + (i >> 2) * 2048 + row * 128 + ((chunk ^ mr) << 4));
+          if (!clean) {
+            vf[0] &= keep_lo;
+            vf[1] &= keep_lo;
+            vf[2] &= keep_hi;
+            vf[3] &= keep_hi;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816<T>(o[nt][i], vf, pf[nt][0], pf[nt][1]);
+        }
+      }
+      ++used;
+      __syncwarp();  // every lane has read the stage
+      produce();
+    }
+    // join the four warps
+#pragma unroll
+    for (int e = 0; e < 2 * NT; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+    }
+    if (!first_segment) __syncthreads();  // the last unit's join has been read
+    first_segment = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (lane < 4) {
+        join_ml[warp * C::ROWS + nt * 8 + 2 * cq] = make_float2(m[2 * nt], l[2 * nt]);
+        join_ml[warp * C::ROWS + nt * 8 + 2 * cq + 1] = make_float2(m[2 * nt + 1], l[2 * nt + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          join_o[(warp * C::ROWS + nt * 8 + 2 * cq + (e & 1)) * C::O_LD + i * 16 + rq + (e >> 1) * 8] = o[nt][i][e];
+    }
+    __syncthreads();
+    const bool begins = w.t0 == 0, ends = w.t1 == w.tiles;
+    const int slot = begins ? 2 * c + 1 : 2 * c;
+    if (begins && !ends && threadIdx.x == 0) {
+      const int64_t line_end = piece_start(pl, c + 1) - w.left + w.tiles;  // behind the unit's last tile (t0 = 0)
+      const int rows = (int)min((int64_t)C::ROWS, (int64_t)w.s.n * a.group - (int64_t)w.rt * C::ROWS);
+      a.desc[c] = make_int4(w.unit, w.head, piece_of(pl, line_end - 1), rows);
+    }
+    constexpr int PER_ROW = D / 4;
+    for (int i = threadIdx.x; i < C::ROWS * PER_ROW; i += DEC_ATTN_THREADS) {
+      const int r = i / PER_ROW, d = (i - r * PER_ROW) * 4;
+      int64_t tok;
+      int head, sn;
+      if (!unit_row(w, a, C::ROWS, r, tok, head, sn)) break;  // rows ascend
+      float2 ml[DEC_ATTN_WARPS];
+      float top = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < DEC_ATTN_WARPS; ++x) {
+        ml[x] = join_ml[x * C::ROWS + r];
+        top = fmaxf(top, ml[x].x);
+      }
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < DEC_ATTN_WARPS; ++x) {
+        const float f = exp2_fast(ml[x].x - ref);
+        const float4 v = *reinterpret_cast<const float4 *>(join_o + (x * C::ROWS + r) * C::O_LD + d);
+        sum = fmaf(f, ml[x].y, sum);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (begins && ends) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        store4<T>(reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh + d,
+                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (a.lse && d == 0)
+          a.lse[tok * a.heads + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        *reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * C::ROWS + r) * D + d) = acc;
+        if (d == 0) a.part_ml[slot * C::ROWS + r] = make_float2(top, sum);
+      }
+    }
+  } while (walk_next(w, bt, a, sh));
+  if (!ok) {  // a wait gave up: let the copies in flight land, then say so
+    if (lane == 0) {
+      for (uint32_t i = used; i < issued; ++i) {
+        mbar_drain(&full[warp][i % C::STAGES][0], (i / C::STAGES) & 1u);
+        mbar_drain(&full[warp][i % C::STAGES][1], (i / C::STAGES) & 1u);
+      }
+      atomicExch(a.status, DCKV_ETIMEOUT);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ joining split units
+// Block (c, y): if a unit begins in worker c's piece and is split, joins its rows y, y + gridDim.y, ...
+// Parts: slot 2 c + 1 (the beginning), then slot 2 i of the workers i up to the last.  Four
+// groups of threads take every fourth part, then add up.
+constexpr int JOIN_THREADS = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const BatchDev bt, const AttnDev a, const AttnShape sh) {
+  constexpr int PER_ROW = D / 4;
+  constexpr int GROUPS = JOIN_THREADS / PER_ROW;
+  __shared__ float4 acc_sm[GROUPS][PER_ROW];
+  __shared__ float sum_sm[GROUPS];
+  const int c = blockIdx.x;
+  const int4 ds = a.desc[c];
+  if (ds.x < 0) return;
+  AttnWalk w;
+  w.head = ds.y;
+  w.unit = ds.x;
+  w.t0 = 0;
+  w.left = 1;
+  walk_load(w, bt, a, sh);
+  const int grp = threadIdx.x / PER_ROW, d4 = threadIdx.x % PER_ROW;
+  const int parts = ds.z - c + 1;
+  for (int r = blockIdx.y; r < ds.w; r += gridDim.y) {
+    float top = -INFINITY;
+    for (int i = 0; i < parts; ++i) {
+      const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
+      top = fmaxf(top, a.part_ml[slot * sh.rows + r].x);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < parts; i += GROUPS) {
+      const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
+      const float2 ml = a.part_ml[slot * sh.rows + r];
+      const float f = exp2_fast(ml.x - ref);
+      const float4 v = *reinterpret_cast<const float4 *>(a.part_o + ((int64_t)slot * sh.rows + r) * D + d4 * 4);
+      sum = fmaf(f, ml.y, sum);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    acc_sm[grp][d4] = acc;
+    if (d4 == 0) sum_sm[grp] = sum;
+    __syncthreads();
+    if (grp == 0) {
+      for (int g = 1; g < GROUPS; ++g) {
+        const float4 v = acc_sm[g][d4];
+        sum += sum_sm[g];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+      int64_t tok;
+      int head, sn;
+      if (unit_row(w, a, sh.rows, r, tok, head, sn)) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        store4<T>(reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh + d4 * 4,
+                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (a.lse && d4 == 0)
+          a.lse[tok * a.heads + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+    __syncthreads();
   }
 }
 
 }  // namespace dckv
 
+// ============================================================================ host
+// One layer of a pool as [pages][heads][page rows][dim]; box: 64 dims x box_rows rows.
+static int map_pages(CUtensorMap *m, const void *ptr, bool bf16, const PoolDev &p, int64_t rs, int64_t hs, int64_t ps,
+                     int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(DCKV_ECUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[4] = {(cuuint64_t)p.dim, (cuuint64_t)p.page_size, (cuuint64_t)p.heads, (cuuint64_t)p.n_pages};
+  // a dimension of one entry has no stride to speak of
+  cuuint64_t strides[3] = {(cuuint64_t)rs * 2, (cuuint64_t)(p.heads > 1 ? hs : 8) * 2,
+                           (cuuint64_t)(p.n_pages > 1 ? ps : 8) * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DCKV_ECUDA, "tensor map (pages) encode failed: %d", (int)r);
+  return DCKV_OK;
+}
+
+struct AttnLayout {
+  size_t part_o, part_ml, desc, total;
+};
+
+static AttnLayout attn_layout(int rows, int dim) {
+  AttnLayout l;
+  l.part_o = 0;
+  l.part_ml = l.part_o + sizeof(float) * 2ull * ATTN_MAX_WORKERS * rows * dim;
+  l.desc = l.part_ml + sizeof(float2) * 2ull * ATTN_MAX_WORKERS * rows;
+  l.total = l.desc + sizeof(int4) * ATTN_MAX_WORKERS;
+  return l;
+}
+
+// Rows of a tile: 8 where every sequence's packed rows fit, else 16.
+static int attn_rows(const BatchDev &b, int group) { return (int64_t)b.max_new * group <= 8 ? 8 : 16; }
+
 extern "C" size_t dckv_attention_workspace_bytes(const dckv_kv_pool *pool, const dckv_cache_batch *batch, int n_q_heads) {
   PoolDev p;
   BatchDev b;
   if (check_pool(pool, p) != DCKV_OK || check_batch(batch, 0, b) != DCKV_OK) return 0;
-  if (n_q_heads < 1 || n_q_heads % p.heads) {
+  if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % p.heads) {
     fail(DCKV_EINVAL, "n_q_heads %d is not a multiple of the pool's heads", n_q_heads);
     return 0;
   }
-  return 256;
+  return attn_layout(attn_rows(b, n_q_heads / p.heads), p.dim).total;
+}
+
+static int sm_count(int device, int &n) {
+  static std::atomic<int> known[64];
+  n = known[device].load();
+  if (n == 0) {
+    CK(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device));
+    known[device].store(n);
+  }
+  return DCKV_OK;
+}
+
+template <typename T, int D, int NT>
+static int run_attend_few(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
+                          const AttnDev &a, const AttnShape &sh, cudaStream_t st) {
+  auto kern = k_attend_few<T, D, NT>;
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeAttn<D, NT>::SMEM));
+  kern<<<a.workers, DEC_ATTN_THREADS, DecodeAttn<D, NT>::SMEM, st>>>(mk, mv, p, b, a, sh);
+  ++g_launches;
+  k_attend_join<T, D><<<dim3(a.workers, 8), JOIN_THREADS, 0, st>>>(b, a, sh);
+  ++g_launches;
+  CK(cudaGetLastError());
+  return DCKV_OK;
+}
+
+template <typename T, int D>
+static int run_attend(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
+                      const AttnDev &a, const AttnShape &sh, cudaStream_t st) {
+  if (sh.rows == 8) return run_attend_few<T, D, 1>(mk, mv, p, b, a, sh, st);
+  return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, st);
 }
 
 extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *batch, const dckv_attention_args *args,
@@ -99,33 +750,41 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   if (args->layer < 0 || args->layer >= p.n_layers) return fail(DCKV_EINVAL, "layer %d out of range", args->layer);
   if (args->causal != 0 && args->causal != 1) return fail(DCKV_EINVAL, "causal must be 0 or 1");
   if (!std::isfinite(args->scale) || !(args->scale > 0.f)) return fail(DCKV_EINVAL, "scale must be finite and positive");
-  AttnDev a{(const char *)args->q, (char *)args->out, args->lse, args->q_token_stride, args->q_head_stride,
-            args->out_token_stride, args->out_head_stride, n, hq, hq / p.heads, args->layer, args->causal, args->scale,
-            status};
-  if (bad_stride(a.qt, n, 8) || bad_stride(a.qh, hq, 8) || bad_stride(a.ot, n, 8) || bad_stride(a.oh, hq, 8))
+  int64_t qt = args->q_token_stride, qh = args->q_head_stride, ot = args->out_token_stride, oh = args->out_head_stride;
+  if (bad_stride(qt, n, 8) || bad_stride(qh, hq, 8) || bad_stride(ot, n, 8) || bad_stride(oh, hq, 8))
     return fail(DCKV_EINVAL, "q and out strides must be positive multiples of 8 elements");
-  if (n <= 1) a.qt = a.ot = 0;
-  if (hq == 1) a.qh = a.oh = 0;
-  if (n > 0 && overlaps(a.q, span_bytes(n, a.qt, hq, a.qh, p.dim, 2), a.out, span_bytes(n, a.ot, hq, a.oh, p.dim, 2)))
+  if (n <= 1) qt = ot = 0;
+  if (hq == 1) qh = oh = 0;
+  if (n > 0 && overlaps(args->q, span_bytes(n, qt, hq, qh, p.dim, 2), args->out, span_bytes(n, ot, hq, oh, p.dim, 2)))
     return fail(DCKV_EINVAL, "out overlaps q");
-  const size_t need = dckv_attention_workspace_bytes(pool, batch, hq);
-  if (ws_bytes < need) return fail(DCKV_ECAPACITY, "workspace too small (%zu < %zu)", ws_bytes, need);
+  const int group = hq / p.heads;
+  AttnShape sh;
+  sh.rows = attn_rows(b, group);
+  sh.key_tile = DEC_KEY_TILE;
+  sh.kv_heads = p.heads;
+  const int64_t row_tiles = ((int64_t)std::min<int64_t>(b.max_new, std::max<int64_t>(n, 1)) * group + sh.rows - 1) / sh.rows;
+  if (row_tiles * b.batch > 0x7fffffffll) return fail(DCKV_EINVAL, "batch times max_new is too large");
+  sh.row_tiles = (int)row_tiles;
+  sh.units = (int)(row_tiles * b.batch);
+  sh.max_slots = std::min<int64_t>((int64_t)b.max_pages * p.page_size, 0x7fffffffll - 65536);
+  const AttnLayout lay = attn_layout(sh.rows, p.dim);
+  if (ws_bytes < lay.total) return fail(DCKV_ECAPACITY, "workspace too small (%zu < %zu)", ws_bytes, lay.total);
   if (n == 0) return DCKV_OK;
   cudaStream_t st = (cudaStream_t)stream;
   DEVICE_SCOPE(pool->device);
+  int sms;
+  RET(sm_count(pool->device, sms));
+  char *ws = (char *)workspace;
+  const AttnDev a{(const char *)args->q, (char *)args->out, args->lse, qt, qh, ot, oh, hq, group, args->causal,
+                  args->scale * 1.4426950408889634f, status, (float *)(ws + lay.part_o), (float2 *)(ws + lay.part_ml),
+                  (int4 *)(ws + lay.desc), std::min(sms, ATTN_MAX_WORKERS)};
   const bool bf = pool->dtype == DCKV_BF16;
-  const unsigned g = (unsigned)n;
-  if (p.dim == 64) {
-    if (bf) k_attend<__nv_bfloat16, 64><<<g, CACHE_THREADS, 0, st>>>(p, b, a);
-    else k_attend<__half, 64><<<g, CACHE_THREADS, 0, st>>>(p, b, a);
-  } else if (p.dim == 128) {
-    if (bf) k_attend<__nv_bfloat16, 128><<<g, CACHE_THREADS, 0, st>>>(p, b, a);
-    else k_attend<__half, 128><<<g, CACHE_THREADS, 0, st>>>(p, b, a);
-  } else {
-    if (bf) k_attend<__nv_bfloat16, 256><<<g, CACHE_THREADS, 0, st>>>(p, b, a);
-    else k_attend<__half, 256><<<g, CACHE_THREADS, 0, st>>>(p, b, a);
-  }
-  ++g_launches;
-  CK(cudaGetLastError());
-  return DCKV_OK;
+  CUtensorMap mk, mv;
+  RET(map_pages(&mk, p.k + 2 * args->layer * p.kl, bf, p, p.kr, p.kh, p.kp, DEC_SLICE));
+  RET(map_pages(&mv, p.v + 2 * args->layer * p.vl, bf, p, p.vr, p.vh, p.vp, DEC_SLICE));
+  if (p.dim == 64)
+    return bf ? run_attend<__nv_bfloat16, 64>(mk, mv, p, b, a, sh, st) : run_attend<__half, 64>(mk, mv, p, b, a, sh, st);
+  if (p.dim == 128)
+    return bf ? run_attend<__nv_bfloat16, 128>(mk, mv, p, b, a, sh, st) : run_attend<__half, 128>(mk, mv, p, b, a, sh, st);
+  return bf ? run_attend<__nv_bfloat16, 256>(mk, mv, p, b, a, sh, st) : run_attend<__half, 256>(mk, mv, p, b, a, sh, st);
 }
