@@ -584,6 +584,431 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------------ many rows: CTA pairs
+// More than 16 packed rows: tcgen05 with cta_group::2.  A pair takes 256 rows (128 per CTA) and
+// walks key tiles of 128: S = Q K^T (M 256, N 128) and O += P V (M 256, N dim), each CTA holding
+// half of K (64 keys, all dims) and half of V (all keys, half the dims).  A CTA alone would
+// stream a whole K and V tile per 128 rows, 128 bytes per clock at the tensor rate and dim 256;
+// the pair needs half of that per SM, what L2 gives.
+// TMEM (512 columns): O in the first `dim`, then two S tiles of 128 columns; P overwrites the
+// first half of its own S tile as 16-bit pairs and is the A operand of the second product.
+// Roles, per CTA: warp 0 loads K and V halves (lanes issue one TMA box each, through the page
+// table), warp 1 of the even CTA issues all MMAs, warps 2-9 are the softmax: two threads per
+// row, 64 columns each, which exchange the row maximum through shared memory.  While they work
+// on tile j the tensor cores run S(j + 1), then O(j).
+// The maximum a row's weights refer to moves only when the true one exceeds it by more than
+// RESCALE_STEPS in log2: until then P stays below 2^RESCALE_STEPS, exactly representable ranges
+// in both types, and O needs no rescaling, which costs a round trip of O through registers.
+constexpr int PAIR_ROWS = 256;
+constexpr int PAIR_KEYS = 128;
+constexpr int PAIR_SOFT_WARPS = 8;
+constexpr int PAIR_THREADS = 64 + 32 * PAIR_SOFT_WARPS;
+constexpr int ATTN_MAX_PAIRS = 80;
+constexpr float RESCALE_STEPS = 8.f;
+
+template <int D>
+struct PairAttn {
+  static constexpr int Q_BYTES = 128 * D * 2;
+  static constexpr int BUF_BYTES = 64 * D * 2;  // half of K, or half of V
+  static constexpr int V_ROW = D >= 128 ? 128 : 64;  // bytes of a V half's row in one block
+  static constexpr int V_BLOCKS = D >= 128 ? D / 128 : 1;
+  static constexpr int AREA = 512 + 2048 + 512;  // barriers, exchange, plan
+  static constexpr int FIT = (232448 - AREA - Q_BYTES) / BUF_BYTES;
+  static constexpr int STAGES = FIT > 10 ? 10 : FIT;
+  static constexpr int SMEM = Q_BYTES + STAGES * BUF_BYTES + AREA;
+  static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory");
+};
+
+template <int STAGES>
+struct PairBars {
+  uint64_t full[STAGES];   // leader: both halves of an item landed
+  uint64_t empty[STAGES];  // both: the item's MMAs are done
+  uint64_t s_full[2];      // both: S tile computed
+  uint64_t p_full[2];      // leader: P written by every softmax warp of the pair
+  uint64_t pv_done;        // both: O += P V of a tile done.  S(j) complete implies O(j - 2) complete, so
+                           // a warp at tile j may wait here for O(j - 1), not for any later one
+  uint64_t o_full;         // both: the unit's last O += P V done
+  uint64_t q_full;         // leader: Q staged by every softmax warp
+  uint64_t o_empty;        // leader: O read by every softmax warp
+  uint64_t fix;            // own: a ragged V half landed
+  GemmTail<STAGES> tail;
+};
+
+struct PairMaps {
+  int k_box, v_box;  // rows of one TMA box
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+    k_attend_many(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PoolDev p,
+                  const BatchDev bt, const AttnDev a, const AttnShape sh, const PairMaps mp) {
+  using C = PairAttn<D>;
+  constexpr int STAGES = C::STAGES;
+  constexpr uint32_t S_COL = 256;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  // no room for slack: the swizzled tiles rely on dynamic shared memory starting on 1,024 bytes
+  // (it does where a kernel has no static shared memory)
+  if (smem_u32(dyn_smem) & 1023u) {
+    if (threadIdx.x == 0) atomicExch(a.status, DCKV_ECUDA);
+    return;
+  }
+  uint8_t *q_sm = dyn_smem;
+  uint8_t *bufs = dyn_smem + C::Q_BYTES;
+  PairBars<STAGES> *bars = reinterpret_cast<PairBars<STAGES> *>(bufs + STAGES * C::BUF_BYTES);
+  static_assert(sizeof(PairBars<STAGES>) <= 512 && sizeof(AttnPlanSmem) <= 512, "barrier area");
+  float *xch = reinterpret_cast<float *>(bufs + STAGES * C::BUF_BYTES + 512);  // [tile parity][half][row]
+  AttnPlanSmem *plan_sm = reinterpret_cast<AttnPlanSmem *>(bufs + STAGES * C::BUF_BYTES + 512 + 2048);
+  GemmTail<STAGES> *tail = &bars->tail;
+  volatile int *abort_flag = &tail->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int c = blockIdx.x >> 1;
+  uint32_t n_issued = 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 2 * PAIR_SOFT_WARPS);
+    }
+    mbar_init(&bars->pv_done, 1);
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->q_full, 2 * PAIR_SOFT_WARPS);
+    mbar_init(&bars->o_empty, 2 * PAIR_SOFT_WARPS);
+    mbar_init(&bars->fix, 1);
+    mbar_init(&tail->drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&tail->tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  AttnPlan pl;
+  AttnWalk w;
+  const bool any = attn_plan<PAIR_THREADS>(bt, a, sh, 1, c, plan_sm, pl, w);
+  if (threadIdx.x == 0 && rank == 0) a.desc[c] = make_int4(-1, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem = tail->tmem_base;
+
+  if (!any) {
+    // no piece: straight to the teardown (both CTAs of the pair alike)
+  } else if (warp == 0) {
+    // ---------------------------------------------------------------- K and V (both CTAs)
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t fixes = 0;
+    bool ok = true;
+    // one item: tile t's K half or V half
+    auto load = [&](const AttnWalk &wk, int t, bool is_v) {
+      const int key0 = t * PAIR_KEYS + (is_v ? 0 : (int)rank * 64);
+      const int box = is_v ? mp.v_box : mp.k_box;
+      const int groups = (is_v ? PAIR_KEYS : 64) / box, blocks = is_v ? C::V_BLOCKS : D / 64;
+      // this lane's box (at most 32): rows from `key`, page and row in it
+      const int g = lane % groups, blk = lane / groups;
+      const int key = key0 + g * box;
+      int page = (int)p.n_pages, row = 0;  // behind the pool: the copy fills zeros
+      if (blk < blocks && key < wk.s.len) {
+        const int pi = key / p.page_size;
+        row = key - pi * p.page_size;
+        page = __ldg(bt.page_table + wk.b * bt.table_stride + pi);
+        if (page < 0 || page >= p.n_pages) {
+          atomicExch(a.status, DCKV_ERANGE);
+          page = (int)p.n_pages;
+          row = 0;
+        }
+      }
+      // a V box that the sequence's last slot ends in: the rows behind it may hold anything, and
+      // 0 * NaN is NaN, so they are cleared before the MMA sees them
+      const int last_box = wk.s.len / box * box;  // first key of the box that holds slot `len`
+      const bool ragged = is_v && wk.s.len % box != 0 && last_box >= key0 && last_box < key0 + PAIR_KEYS;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag));
+      if (!ok) return;
+      uint8_t *dst = bufs + stage * C::BUF_BYTES;
+      const uint32_t fb = mapa_shared(smem_u32(&bars->full[stage]), 0);
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(&bars->full[stage], 2 * C::BUF_BYTES);
+        if (ragged) mbar_arrive_expect_tx(&bars->fix, C::BUF_BYTES);
+        tail->ring[stage] = C::BUF_BYTES;
+        ++n_issued;
+      }
+      __syncwarp();
+      if (blk < blocks) {
+        if (!is_v) {
+          tma_load_4d_pair(dst + blk * 8192 + g * box * 128, &tm_k, fb, 64 * blk, row, wk.head, page);
+        } else {
+          uint8_t *to = dst + (blk * PAIR_KEYS + g * box) * C::V_ROW;
+          const int d0 = (int)rank * (D / 2) + blk * 64;
+          if (ragged) tma_load_4d(to, &tm_v, &bars->fix, d0, row, wk.head, page);
+          else tma_load_4d_pair(to, &tm_v, fb, d0, row, wk.head, page);
+        }
+      }
+      if (ragged) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->fix, fixes & 1u, abort_flag));
+        if (!ok) mbar_drain(&bars->fix, fixes & 1u);
+        ++fixes;
+        const int r0 = wk.s.len - key0, n = (last_box + box - wk.s.len) * (C::V_ROW / 16);
+        for (int i = lane; i < n * C::V_BLOCKS; i += 32) {
+          const int b = i / n, j = i - b * n;
+          reinterpret_cast<uint4 *>(dst + (b * PAIR_KEYS + r0) * C::V_ROW)[j] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_complete_tx_cluster(fb, C::BUF_BYTES);
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    do {
+      load(w, w.t0, false);
+      for (int t = w.t0; t < w.t1 && ok; ++t) {
+        if (t + 1 < w.t1) load(w, t + 1, false);
+        if (ok) load(w, t, true);
+      }
+    } while (ok && walk_next(w, bt, a, sh));
+    // every stage released: no commit is still in flight towards this CTA when it exits
+    for (int i = 0; i < STAGES && ok; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (even CTA)
+    if (lane == 0 && rank == 0) {
+      constexpr int BF = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+      const uint32_t id_s = idesc_f16(BF, PAIR_ROWS, PAIR_KEYS);
+      const uint32_t id_o = idesc_f16(BF, PAIR_ROWS, D) | IDESC_B_MN_MAJOR;
+      const uint32_t q0 = smem_u32(q_sm);
+      int stage = 0;
+      uint32_t phase = 0, tile = 0, item = 0;
+      bool ok = true;
+      auto scores = [&](uint32_t j) {  // S tile j of the kernel
+        ok = mbar_wait(&bars->full[stage], phase, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t kb = smem_u32(bufs + stage * C::BUF_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16_pair(tmem + S_COL + (j & 1u) * PAIR_KEYS, sw128_desc(q0 + (kk >> 2) * 16384 + (kk & 3) * 32),
+                        sw128_desc(kb + (kk >> 2) * 8192 + (kk & 3) * 32), id_s, kk > 0);
+        umma_commit_pair(&bars->empty[stage]);
+        umma_commit_pair(&bars->s_full[j & 1u]);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      do {
+        ok = mbar_wait_cluster(&bars->q_full, item & 1u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        scores(tile);
+        const int n = w.t1 - w.t0;
+        for (int t = 0; t < n && ok; ++t, ++tile) {
+          if (t + 1 < n) scores(tile + 1);
+          if (ok && t == 0 && item > 0) ok = mbar_wait_cluster(&bars->o_empty, (item - 1) & 1u, abort_flag);
+          if (ok) ok = mbar_wait_cluster(&bars->p_full[tile & 1u], (tile >> 1) & 1u, abort_flag);
+          if (ok) ok = mbar_wait_cluster(&bars->full[stage], phase, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t vb = smem_u32(bufs + stage * C::BUF_BYTES);
+          const uint32_t pt = tmem + S_COL + (tile & 1u) * PAIR_KEYS;
+#pragma unroll
+          for (int kk = 0; kk < PAIR_KEYS / 16; ++kk)
+            umma_f16_pair_ts(tmem, pt + kk * 8, mn_desc(vb + kk * 16 * C::V_ROW, C::V_ROW, PAIR_KEYS * C::V_ROW), id_o,
+                             t > 0 || kk > 0);
+          umma_commit_pair(&bars->empty[stage]);
+          umma_commit_pair(&bars->pv_done);
+          if (t + 1 == n) umma_commit_pair(&bars->o_full);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        ++item;
+      } while (ok && walk_next(w, bt, a, sh));
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax (both CTAs)
+    const int sw = warp - 2, quarter = warp & 3, half = sw >> 2;
+    const int row = quarter * 32 + lane;  // of this CTA's 128
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t l_p[2] = {mapa_shared(smem_u32(&bars->p_full[0]), 0), mapa_shared(smem_u32(&bars->p_full[1]), 0)};
+    const uint32_t l_q = mapa_shared(smem_u32(&bars->q_full), 0);
+    const uint32_t l_o = mapa_shared(smem_u32(&bars->o_empty), 0);
+    bool ok = true;
+    uint32_t tile = 0, item = 0;
+
+    auto stage_q = [&](const AttnWalk &wk) {  // this CTA's 128 rows of Q, 16 rows per warp
+      constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks per row, rows per step
+      const int ch = lane % CH;
+#pragma unroll 8
+      for (int r0 = 0; r0 < 16; r0 += RPI) {
+        const int r = sw * 16 + r0 + lane / CH;
+        int64_t tok;
+        int head, sn;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (unit_row(wk, a, PAIR_ROWS, (int)rank * 128 + r, tok, head, sn))
+          v = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(a.q) + tok * a.qt + head * a.qh) + ch);
+        *reinterpret_cast<uint4 *>(q_sm + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_release(l_q);
+    };
+    stage_q(w);
+    bool more = true;
+    do {
+      int64_t tok = 0;
+      int head = 0, seen = 0x7fffffff;
+      const bool valid = unit_row(w, a, PAIR_ROWS, (int)rank * 128 + row, tok, head, seen);
+      if (!valid) seen = 0x7fffffff;
+      const bool work = __any_sync(0xffffffffu, valid);  // the same in both halves of the rows
+      float ref = -INFINITY, sum = 0.f;  // ref in log2 units
+      for (int t = w.t0; t < w.t1; ++t, ++tile) {
+        const uint32_t sb = lanes + S_COL + (tile & 1u) * PAIR_KEYS;
+        if (ok) ok = mbar_wait(&bars->s_full[tile & 1u], (tile >> 1) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        if (work) {
+          uint32_t x[64];
+          tmem_ld_32x32b_x32(sb + half * 64, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld_32x32b_x32(sb + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+          tmem_ld_wait();
+          const int limit = seen - t * PAIR_KEYS - half * 64;  // columns from here on are masked
+          if (__any_sync(0xffffffffu, limit < 64)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= limit) x[i] = 0xff800000u;  // -infinity
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[i]));
+          const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+          float *xc = xch + (tile & 1u) * 256;
+          xc[half * 128 + row] = mine;
+          named_bar_sync(1 + quarter, 64);
+          const float top = fmaxf(mine, xc[(half ^ 1) * 128 + row]);
+          const bool move = top > ref + RESCALE_STEPS;
+          if (__any_sync(0xffffffffu, move)) {
+            const float next = move ? top : ref;
+            const float f = move ? exp2_fast(ref - next) : 1.f;
+            sum *= f;
+            ref = next;
+            if (t > w.t0) {  // O of the tiles before: this half's columns
+              if (ok) ok = mbar_wait(&bars->pv_done, (tile - 1) & 1u, abort_flag);
+              ok = __all_sync(0xffffffffu, ok);
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(lanes + d, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_32x32b_x32(lanes + d, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          const float off = ref == -INFINITY ? 0.f : -ref;
+          uint32_t pk[32];
+          float s2[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float e0 = exp2_fast(fmaf(__uint_as_float(x[2 * i]), a.scale_log2, off));
+            const float e1 = exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), a.scale_log2, off));
+            s2[0] += e0;
+            s2[1] += e1;
+            pk[i] = pack2<T>(e0, e1);
+          }
+          sum += s2[0] + s2[1];
+          tmem_st_32x32b_x32(sb + half * 32, pk);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_release(l_p[tile & 1u]);
+      }
+      // every S of this unit is computed, so Q may be replaced
+      AttnWalk nw = w;
+      more = walk_next(nw, bt, a, sh);
+      if (more) stage_q(nw);
+      // the unit's end: join the halves' sums, read O
+      float *xc = xch + (tile & 1u) * 256;
+      xc[half * 128 + row] = sum;
+      named_bar_sync(1 + quarter, 64);
+      sum += xc[(half ^ 1) * 128 + row];
+      if (ok) ok = mbar_wait(&bars->o_full, item & 1u, abort_flag);
+      ++item;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      named_bar_sync(1 + quarter, 64);  // sums read before the next unit's maxima overwrite them
+      const bool begins = w.t0 == 0, ends = w.t1 == w.tiles;
+      const int slot = begins ? 2 * c + 1 : 2 * c;
+      const float inv = begins && ends ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+      if (work) {
+        const int64_t part = (int64_t)slot * PAIR_ROWS + rank * 128 + row;
+#pragma unroll 1
+        for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(lanes + d, o);
+          tmem_ld_wait();
+          if (!valid || !ok) {
+          } else if (begins && ends) {
+            T *out = reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh + d;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 v;
+              v.x = pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+              v.y = pack2<T>(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+              v.z = pack2<T>(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+              v.w = pack2<T>(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+              *reinterpret_cast<uint4 *>(out + i) = v;
+            }
+          } else {
+            float *out = a.part_o + part * D + d;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4 *>(out + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+        if (valid && half == 0 && ok) {
+          if (!(begins && ends)) a.part_ml[part] = make_float2(ref, sum);
+          else if (a.lse) a.lse[tok * a.heads + head] = sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      if (begins && !ends && rank == 0 && sw == 0 && lane == 0) {
+        const int64_t line_end = piece_start(pl, c + 1) - w.left + w.tiles;
+        const int rows = (int)min((int64_t)PAIR_ROWS, (int64_t)w.s.n * a.group - (int64_t)w.rt * PAIR_ROWS);
+        a.desc[c] = make_int4(w.unit, w.head, piece_of(pl, line_end - 1), rows);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_release(l_o);
+      w = nw;
+    } while (more);
+  }
+  __syncthreads();
+  pair_teardown<STAGES>(tail, bars->full, n_issued, rank, warp, lane, a.status);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // ------------------------------------------------------------------ joining split units
 // Block (c, y): if a unit begins in worker c's piece and is split, joins its rows y, y + gridDim.y, ...
 // Parts: slot 2 c + 1 (the beginning), then slot 2 i of the workers i up to the last.  Four
@@ -657,20 +1082,21 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const BatchDev bt,
 }  // namespace dckv
 
 // ============================================================================ host
-// One layer of a pool as [pages][heads][page rows][dim]; box: 64 dims x box_rows rows.
+// One layer of a pool as [pages][heads][page rows][dim]; box: 64 (or 32) dims x box_rows rows,
+// swizzled by its row's bytes.
 static int map_pages(CUtensorMap *m, const void *ptr, bool bf16, const PoolDev &p, int64_t rs, int64_t hs, int64_t ps,
-                     int box_rows) {
+                     int box_rows, int box_dims = 64) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(DCKV_ECUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[4] = {(cuuint64_t)p.dim, (cuuint64_t)p.page_size, (cuuint64_t)p.heads, (cuuint64_t)p.n_pages};
   // a dimension of one entry has no stride to speak of
   cuuint64_t strides[3] = {(cuuint64_t)rs * 2, (cuuint64_t)(p.heads > 1 ? hs : 8) * 2,
                            (cuuint64_t)(p.n_pages > 1 ? ps : 8) * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t box[4] = {(cuuint32_t)box_dims, (cuuint32_t)box_rows, 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  box_dims == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DCKV_ECUDA, "tensor map (pages) encode failed: %d", (int)r);
   return DCKV_OK;
 }
@@ -680,16 +1106,21 @@ struct AttnLayout {
 };
 
 static AttnLayout attn_layout(int rows, int dim) {
+  const int workers = rows == PAIR_ROWS ? ATTN_MAX_PAIRS : ATTN_MAX_WORKERS;
   AttnLayout l;
   l.part_o = 0;
-  l.part_ml = l.part_o + sizeof(float) * 2ull * ATTN_MAX_WORKERS * rows * dim;
-  l.desc = l.part_ml + sizeof(float2) * 2ull * ATTN_MAX_WORKERS * rows;
-  l.total = l.desc + sizeof(int4) * ATTN_MAX_WORKERS;
+  l.part_ml = l.part_o + sizeof(float) * 2ull * workers * rows * dim;
+  l.desc = l.part_ml + sizeof(float2) * 2ull * workers * rows;
+  l.total = l.desc + sizeof(int4) * workers;
   return l;
 }
 
-// Rows of a tile: 8 where every sequence's packed rows fit, else 16.
-static int attn_rows(const BatchDev &b, int group) { return (int64_t)b.max_new * group <= 8 ? 8 : 16; }
+// Rows of a tile: 8 or 16 where every sequence's packed rows fit (k_attend_few), else a pair's
+// 256 (k_attend_many).
+static int attn_rows(const BatchDev &b, int group) {
+  const int64_t rows = (int64_t)b.max_new * group;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : PAIR_ROWS;
+}
 
 extern "C" size_t dckv_attention_workspace_bytes(const dckv_kv_pool *pool, const dckv_cache_batch *batch, int n_q_heads) {
   PoolDev p;
@@ -726,10 +1157,32 @@ static int run_attend_few(const CUtensorMap &mk, const CUtensorMap &mv, const Po
 }
 
 template <typename T, int D>
+static int run_attend_many(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
+                           const AttnDev &a, const AttnShape &sh, const PairMaps &mp, cudaStream_t st) {
+  auto kern = k_attend_many<T, D>;
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairAttn<D>::SMEM));
+  void *args[] = {(void *)&mk, (void *)&mv, (void *)&p, (void *)&b, (void *)&a, (void *)&sh, (void *)&mp};
+  RET(launch_pairs((const void *)kern, a.workers, 2 * a.workers, PAIR_THREADS, PairAttn<D>::SMEM, st, args));
+  k_attend_join<T, D><<<dim3(a.workers, 32), JOIN_THREADS, 0, st>>>(b, a, sh);
+  ++g_launches;
+  CK(cudaGetLastError());
+  return DCKV_OK;
+}
+
+template <typename T, int D>
 static int run_attend(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
-                      const AttnDev &a, const AttnShape &sh, cudaStream_t st) {
+                      const AttnDev &a, const AttnShape &sh, const PairMaps &mp, cudaStream_t st) {
   if (sh.rows == 8) return run_attend_few<T, D, 1>(mk, mv, p, b, a, sh, st);
-  return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, st);
+  if (sh.rows == 16) return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, st);
+  return run_attend_many<T, D>(mk, mv, p, b, a, sh, mp, st);
+}
+
+// Rows of a TMA box: the largest power of two up to `most` that divides a page, so that no box
+// crosses a page (pages are multiples of 16).
+static int box_rows(int page_size, int most) {
+  int r = 16;
+  while (r < most && page_size % (2 * r) == 0) r *= 2;
+  return r;
 }
 
 extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *batch, const dckv_attention_args *args,
@@ -760,7 +1213,8 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   const int group = hq / p.heads;
   AttnShape sh;
   sh.rows = attn_rows(b, group);
-  sh.key_tile = DEC_KEY_TILE;
+  const bool many = sh.rows == PAIR_ROWS;
+  sh.key_tile = many ? PAIR_KEYS : DEC_KEY_TILE;
   sh.kv_heads = p.heads;
   const int64_t row_tiles = ((int64_t)std::min<int64_t>(b.max_new, std::max<int64_t>(n, 1)) * group + sh.rows - 1) / sh.rows;
   if (row_tiles * b.batch > 0x7fffffffll) return fail(DCKV_EINVAL, "batch times max_new is too large");
@@ -777,14 +1231,19 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   char *ws = (char *)workspace;
   const AttnDev a{(const char *)args->q, (char *)args->out, args->lse, qt, qh, ot, oh, hq, group, args->causal,
                   args->scale * 1.4426950408889634f, status, (float *)(ws + lay.part_o), (float2 *)(ws + lay.part_ml),
-                  (int4 *)(ws + lay.desc), std::min(sms, ATTN_MAX_WORKERS)};
+                  (int4 *)(ws + lay.desc),
+                  many ? std::min(sms / 2, ATTN_MAX_PAIRS) : std::min(sms, ATTN_MAX_WORKERS)};
   const bool bf = pool->dtype == DCKV_BF16;
   CUtensorMap mk, mv;
-  RET(map_pages(&mk, p.k + 2 * args->layer * p.kl, bf, p, p.kr, p.kh, p.kp, DEC_SLICE));
-  RET(map_pages(&mv, p.v + 2 * args->layer * p.vl, bf, p, p.vr, p.vh, p.vp, DEC_SLICE));
+  const PairMaps mp{many ? box_rows(p.page_size, 64) : DEC_SLICE, many ? box_rows(p.page_size, PAIR_KEYS) : DEC_SLICE};
+  RET(map_pages(&mk, p.k + 2 * args->layer * p.kl, bf, p, p.kr, p.kh, p.kp, mp.k_box));
+  RET(map_pages(&mv, p.v + 2 * args->layer * p.vl, bf, p, p.vr, p.vh, p.vp, mp.v_box, many && p.dim == 64 ? 32 : 64));
   if (p.dim == 64)
-    return bf ? run_attend<__nv_bfloat16, 64>(mk, mv, p, b, a, sh, st) : run_attend<__half, 64>(mk, mv, p, b, a, sh, st);
+    return bf ? run_attend<__nv_bfloat16, 64>(mk, mv, p, b, a, sh, mp, st)
+              : run_attend<__half, 64>(mk, mv, p, b, a, sh, mp, st);
   if (p.dim == 128)
-    return bf ? run_attend<__nv_bfloat16, 128>(mk, mv, p, b, a, sh, st) : run_attend<__half, 128>(mk, mv, p, b, a, sh, st);
-  return bf ? run_attend<__nv_bfloat16, 256>(mk, mv, p, b, a, sh, st) : run_attend<__half, 256>(mk, mv, p, b, a, sh, st);
+    return bf ? run_attend<__nv_bfloat16, 128>(mk, mv, p, b, a, sh, mp, st)
+              : run_attend<__half, 128>(mk, mv, p, b, a, sh, mp, st);
+  return bf ? run_attend<__nv_bfloat16, 256>(mk, mv, p, b, a, sh, mp, st)
+            : run_attend<__half, 256>(mk, mv, p, b, a, sh, mp, st);
 }

@@ -83,6 +83,34 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
+// The same wait with cluster scope: what the peer CTA wrote before its release arrive (to its
+// own shared memory or TMEM) is ordered before the operations after this wait.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, "
+      "1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  uint32_t n = 0;
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((++n & 255u) == 0) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 > DCKV_WAIT_NS) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // Bounded wait that ignores the abort flag, for a CTA about to leave after a timeout: it
 // waits (at most another DCKV_WAIT_NS) for the copies it issued itself to land, so that it
 // does not exit while they may still be writing its shared memory.
@@ -223,6 +251,21 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr) {
   return d;
 }
 
+// Descriptor of a B operand stored MN-major (N contiguous) with a swizzle of `row_bytes` = 128
+// or 64: rows of one K index hold row_bytes / 2 elements of N, atoms of 8 rows; the stride byte
+// offset is that of the next 8 K indices, the leading byte offset that of the next
+// row_bytes / 2 elements of N.  Atom bases aligned to 8 * row_bytes.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr, uint32_t row_bytes, uint32_t n_block_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((n_block_bytes >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((8 * row_bytes) >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)(row_bytes == 128 ? 2u : 4u) << 61;
+  return d;
+}
+constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;  // added to idesc_f16 for such a B
+
 // Instruction descriptor, kind::f16: fp32 accumulator (bits 4-5 = 1), A and B type
 // (bits 7-9 / 10-12: 0 = fp16, 1 = bf16), both K-major, N >> 3 in bits 17-22,
 // M >> 4 in bits 24-28.
@@ -293,6 +336,29 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const void *tmap, ui
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const void *tmap, uint32_t bar_cl, int c0, int c1, int c2,
+                                                 int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, "
+      "%5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(bar_cl), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// Arrive with release at cluster scope (see mbar_wait_cluster), own CTA or peer.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cl_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
+}
+
+// Completes `bytes` of the transaction count of an mbarrier in either CTA of the cluster, after
+// everything this thread wrote (the thread's shared-memory writes included).
+__device__ __forceinline__ void mbar_complete_tx_cluster(uint32_t cl_addr, uint32_t bytes) {
+  asm volatile("fence.acq_rel.cluster;\n\tmbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(
+                   cl_addr),
+               "r"(bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                "r"(ncols)
@@ -311,6 +377,16 @@ __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a_desc, 
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with A in TMEM: 16-bit elements, two to a column, one lane per row of A.
+__device__ __forceinline__ void umma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 

@@ -344,6 +344,16 @@ def test_attention_long_axis(dim, length, new):
     check_attention(c, [new], 2, causal=False)
 
 
+@pytest.mark.parametrize("dim,dtype,group,page", [(256, BF16, 4, 64), (128, FP16, 3, 16), (64, BF16, 5, 48)])
+def test_attention_many_tiles_per_block(dim, dtype, group, page):
+    """Enough slots that a block walks several key tiles and several sequences; row counts that
+    leave one row, or none, in a block's warps."""
+    lens, news = [1577, 1416, 926, 2099, 1820, 700, 1501], [77, 33, 43, 31, 21, 129 // group, 0]
+    c = Paged(57, lens, 1, 4, dim, page, "token", dtype)
+    check_attention(c, news, 4 * group)
+    check_attention(c, [1] * 7, 4 * group)
+
+
 @pytest.mark.parametrize("dim,new", [(256, 1), (128, 40), (256, 200)])
 def test_attention_large_scores(dim, new):
     """Scores far beyond exp's range (the running maximum moves, weights underflow)."""
