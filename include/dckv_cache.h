@@ -73,12 +73,22 @@ int dckv_rope_init(dckv_rope_spec *out, int rotary_dim, int layout, double base,
                    double original_len, double low, double high, double magnitude);
 
 /* Rotates x [n_tokens][n_heads][head_dim] (DCKV_BF16, DCKV_FP16 or DCKV_FP32; fp32
- * arithmetic, one rounding) by positions int32 [n_tokens] (any int32; device) into out, same
- * shape and type.  out may be x itself with x's strides (in place); otherwise the byte ranges
- * that x and out span must not overlap.  n_tokens, n_heads up to 2^31 - 1 and 65,535. */
-int dckv_rope(const dckv_rope_spec *spec, int mode, int device, int dtype, const void *x, int64_t x_token_stride,
-              int64_t x_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride, int64_t n_tokens,
-              int n_heads, int head_dim, const int32_t *positions, void *stream);
+ * arithmetic, one rounding) by positions (any int32) into out, same shape and type.  out may be x
+ * itself with x's strides (in place); otherwise the byte ranges that x and out span must not
+ * overlap. */
+typedef struct {
+  const void *x; /* device, aligned to its elements                                        */
+  void *out;
+  int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
+  int64_t n_tokens; /* up to 2^31 - 1                                                      */
+  int32_t n_heads;  /* up to 65,535                                                        */
+  int32_t head_dim; /* rotary_dim .. 65,536                                                */
+  const int32_t *positions; /* device int32 [n_tokens]                                     */
+  int32_t dtype;
+  int32_t device;
+} dckv_rope_args;
+
+int dckv_rope(const dckv_rope_spec *spec, int mode, const dckv_rope_args *args, void *stream);
 
 /* ---- the paged cache ---- */
 

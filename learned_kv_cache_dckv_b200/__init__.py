@@ -78,6 +78,14 @@ class RopeSpec(ctypes.Structure):
                 ("freq", ctypes.c_double * 128)]
 
 
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("x_token_stride", "x_head_stride", "out_token_stride", "out_head_stride",
+                                      "n_tokens")] + [
+        ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("positions", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32), ("device", ctypes.c_int32)]
+
+
 class KvPool(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
         (n, ctypes.c_int32) for n in ("device", "dtype", "n_layers", "n_kv_heads", "head_dim", "page_size")] + [
@@ -145,8 +153,7 @@ def lib():
         "dckv_fit_scales_accumulate": (I, [P, P, P, P, I, P, P, P, Z, P]),
         "dckv_fit_scales_finish": (I, [P, P, P, P]),
         "dckv_rope_init": (I, [P, I, I, ctypes.c_double, I] + [ctypes.c_double] * 5),
-        "dckv_rope": (I, [P, I, I, I, P, ctypes.c_int64, ctypes.c_int64, P, ctypes.c_int64, ctypes.c_int64,
-                          ctypes.c_int64, I, I, P, P]),
+        "dckv_rope": (I, [P, I, P, P]),
         "dckv_cache_append": (I, [P, P, P, P, P, P]),
         "dckv_cache_rows": (I, [P, P, P, P, ctypes.c_int64, ctypes.c_int64, P, P, P]),
         "dckv_attention_workspace_bytes": (Z, [P, P, I]),
@@ -377,43 +384,62 @@ def dckv_fit_scales_finish(handle, abs_sum, laplace_b, stream=None):
 
 
 # ---------------------------------------------------- paged cache and attention (dckv_cache.h)
+# These calls run once per layer and step, so the checks below read each tensor's properties once.
+_CODES = {}  # torch types by element type code, filled on first use
+
+
 def _bad(what):
     raise DckvError(DCKV_EINVAL, what)
 
 
 def _dtype_code(t):
-    import torch
+    if not _CODES:
+        import torch
 
-    code = {torch.bfloat16: DCKV_BF16, torch.float16: DCKV_FP16, torch.float32: DCKV_FP32}.get(t.dtype)
+        _CODES.update({torch.bfloat16: DCKV_BF16, torch.float16: DCKV_FP16, torch.float32: DCKV_FP32,
+                       torch.int32: "int32"})
+    code = _CODES.get(t.dtype)
     if code is None:
         _bad(f"type {t.dtype} is not supported")
     return code
 
 
-def _cuda_check(device, **tensors):
-    """Every tensor given sits on CUDA device `device` with a contiguous last dimension."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda or t.device.index != device:
-            _bad(f"{name} is on {t.device}, not on cuda:{device}")
-        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            _bad(f"the last dimension of {name} must be contiguous")
+def _on(device, name, t):
+    """t's strides, having checked that it sits on that CUDA device and that its last dimension is
+    contiguous."""
+    if t.get_device() != device or device < 0:
+        _bad(f"{name} is on {t.device}, not on cuda:{max(device, 0)}")
+    st = t.stride()
+    if st and st[-1] != 1 and t.shape[-1] > 1:
+        _bad(f"the last dimension of {name} must be contiguous")
+    return st
 
 
-def _int32_check(**tensors):
-    import torch
+def _int32_on(device, name, t):
+    if t.get_device() != device or device < 0:
+        _bad(f"{name} is on {t.device}, not on cuda:{max(device, 0)}")
+    if _dtype_code(t) != "int32":
+        _bad(f"{name} must be int32, not {t.dtype}")
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    for name, t in tensors.items():
-        if t is not None and t.dtype != torch.int32:
-            _bad(f"{name} must be int32, not {t.dtype}")
+
+_raw_stream = None
 
 
 def _device_stream(device, stream):
     """The given stream, or the current one of that device (not of the current device)."""
-    import torch
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
 
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        # the handle without a Stream object around it, where this torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 def rope_spec(rotary_dim, layout="half", base=1.0e7, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=32.0,
@@ -433,22 +459,24 @@ def rope_spec(rotary_dim, layout="half", base=1.0e7, scaling="none", factor=1.0,
 def dckv_rope(spec, x, positions, out, mode="forward", stream=None):
     """Rotates x [n, heads, dim] (bf16, fp16 or fp32) by positions int32 [n] into out (which may
     be x).  mode "forward", "gradient" (the transpose) or "inverse"."""
-    if mode not in ROPE_MODES:
-        _bad(f"unknown rotary mode {mode!r}")
-    if x.dim() != 3 or out.shape != x.shape or positions.shape != x.shape[:1]:
+    shape = x.shape
+    if len(shape) != 3 or out.shape != shape or positions.shape != shape[:1]:
         _bad("x and out must be [n, heads, dim] alike and positions [n]")
-    if out.dtype != x.dtype:
-        _bad("out must have x's type")
-    dev = x.device.index
-    _cuda_check(dev, x=x, out=out, positions=positions)
-    _int32_check(positions=positions)
-    n, heads, dim = x.shape
-    if n == 0:
+    code = _dtype_code(x)
+    if out.dtype != x.dtype or code == "int32":
+        _bad("x and out must have one type, bf16, fp16 or fp32")
+    m = ROPE_MODES.get(mode)
+    if m is None:
+        _bad(f"unknown rotary mode {mode!r}")
+    dev = x.get_device()
+    xs, os_ = _on(dev, "x", x), _on(dev, "out", out)
+    pos = _int32_on(dev, "positions", positions)
+    if shape[0] == 0:
         return out
-    xs, os_ = x.stride(), out.stride()
-    _check(lib().dckv_rope(ctypes.byref(spec), ROPE_MODES[mode], dev, _dtype_code(x), x.data_ptr(), xs[0], xs[1],
-                           out.data_ptr(), os_[0], os_[1], n, heads, dim, positions.data_ptr(),
-                           _device_stream(dev, stream)), "dckv_rope")
+    a = _RopeArgs(x.data_ptr(), out.data_ptr(), xs[0], xs[1], os_[0], os_[1], *shape, pos, code, dev)
+    r = lib().dckv_rope(ctypes.byref(spec), m, ctypes.byref(a), _device_stream(dev, stream))
+    if r:
+        _check(r, "dckv_rope")
     return out
 
 
@@ -459,12 +487,15 @@ def kv_pool(k, v) -> KvPool:
         k, v = k[None], v[None]
     if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype:
         _bad("k and v must be [layers, pages, rows, heads, dim] alike")
-    dev = k.device.index
-    _cuda_check(dev, k=k, v=v)
-    ks, vs = k.stride(), v.stride()
-    p = KvPool(k.data_ptr(), v.data_ptr(), dev, _dtype_code(k), k.shape[0], k.shape[3], k.shape[4], k.shape[2],
-               k.shape[1], *ks[:4], *vs[:4])
+    dev, code = k.get_device(), _dtype_code(k)
+    ks, vs = _on(dev, "k", k), _on(dev, "v", v)
+    if code not in (DCKV_BF16, DCKV_FP16):
+        _bad("pool type must be bf16 or fp16")
+    L, pages, rows, heads, dim = k.shape
+    p = KvPool(k.data_ptr(), v.data_ptr(), dev, code, L, heads, dim, rows, pages, *ks[:4], *vs[:4])
     p.tensors = (k, v)
+    # what the calls below compare with (a ctypes field is slower to read)
+    p.dev, p.code, p.kv_shape, p.dim, p.ref = dev, code, (L, heads, dim), dim, ctypes.byref(p)
     return p
 
 
@@ -475,21 +506,21 @@ def cache_batch(offsets, kv_lens, page_table, max_new) -> CacheBatch:
     if kv_lens.dim() != 1 or offsets.shape != (kv_lens.shape[0] + 1,) or page_table.dim() != 2 or \
             page_table.shape[0] != kv_lens.shape[0]:
         _bad("offsets, kv_lens and page_table must be [batch + 1], [batch] and [batch, pages]")
-    dev = offsets.device.index
-    _cuda_check(dev, offsets=offsets, kv_lens=kv_lens, page_table=page_table)
-    _int32_check(offsets=offsets, kv_lens=kv_lens, page_table=page_table)
-    b = CacheBatch(kv_lens.shape[0], int(max_new), page_table.shape[1], 0, offsets.data_ptr(), kv_lens.data_ptr(),
-                   page_table.data_ptr(), page_table.stride(0))
+    dev = offsets.get_device()
+    st = _on(dev, "page_table", page_table)
+    if _dtype_code(page_table) != "int32":
+        _bad("page_table must be int32")
+    b = CacheBatch(kv_lens.shape[0], int(max_new), page_table.shape[1], 0, _int32_on(dev, "offsets", offsets),
+                   _int32_on(dev, "kv_lens", kv_lens), page_table.data_ptr(), st[0])
     b.tensors = (offsets, kv_lens, page_table)
-    b.device = dev
+    b.dev, b.ref = dev, ctypes.byref(b)
     return b
 
 
-def _pool_check(pool, batch, status, **tensors):
-    if batch.device != pool.device:
-        _bad(f"the batch is on cuda:{batch.device}, the pool on cuda:{pool.device}")
-    _cuda_check(pool.device, status=status, **tensors)
-    _int32_check(status=status)
+def _same_device(pool, batch, status):
+    if batch.dev != pool.dev:
+        _bad(f"the batch is on cuda:{batch.dev}, the pool on cuda:{pool.dev}")
+    return _int32_on(pool.dev, "status", status)
 
 
 def dckv_cache_append(pool, batch, k, v, status, rope=None, positions=None, q=None, q_out=None, stream=None):
@@ -497,59 +528,67 @@ def dckv_cache_append(pool, batch, k, v, status, rope=None, positions=None, q=No
     by `rope` if given; q [n, q heads, dim] rotated into q_out beside them."""
     if k.dim() == 3:
         k, v = k[None], v[None]
-    n = k.shape[1]
-    if k.shape != (pool.n_layers, n, pool.n_kv_heads, pool.head_dim) or v.shape != k.shape:
+    shape, dev, code = k.shape, pool.dev, pool.code
+    if len(shape) != 4 or (shape[0], shape[2], shape[3]) != pool.kv_shape or v.shape != shape:
         _bad("k and v must be [layers, n, heads, dim] of the pool")
-    if _dtype_code(k) != pool.dtype or v.dtype != k.dtype:
+    if _dtype_code(k) != code or v.dtype != k.dtype:
         _bad("k and v must have the pool's type")
-    _pool_check(pool, batch, status, k=k, v=v, positions=positions, q=q, q_out=q_out)
-    ks, vs = k.stride(), v.stride()
-    a = _AppendArgs(k.data_ptr(), v.data_ptr(), *ks[:3], *vs[:3])
-    a.n_tokens = n
-    if positions is not None:
-        _int32_check(positions=positions)
-        if positions.shape != (n,):
-            _bad("positions must be [n]")
-        a.positions = positions.data_ptr()
+    n = shape[1]
+    st = _same_device(pool, batch, status)
+    ks, vs = _on(dev, "k", k), _on(dev, "v", v)
+    qp = op = pos = None
+    qs = os_ = (0, 0)
+    hq = 0
     if q is not None:
-        if q_out is None or q.dim() != 3 or q.shape[0] != n or q.shape[2] != pool.head_dim or q_out.shape != q.shape:
+        qshape = q.shape
+        if q_out is None or len(qshape) != 3 or qshape[0] != n or qshape[2] != pool.dim or q_out.shape != qshape:
             _bad("q and q_out must be [n, q heads, dim]")
         if q.dtype != k.dtype or q_out.dtype != k.dtype:
             _bad("q and q_out must have the pool's type")
-        a.q, a.q_out, a.n_q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-        a.q_token_stride, a.q_head_stride = q.stride()[:2]
-        a.q_out_token_stride, a.q_out_head_stride = q_out.stride()[:2]
+        qs, os_, hq = _on(dev, "q", q), _on(dev, "q_out", q_out), qshape[1]
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         _bad("q_out without q")
+    if positions is not None:
+        if positions.shape != (n,):
+            _bad("positions must be [n]")
+        pos = _int32_on(dev, "positions", positions)
     if n == 0:
         return
-    _check(lib().dckv_cache_append(ctypes.byref(pool), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
-                                   ctypes.byref(a), status.data_ptr(), _device_stream(pool.device, stream)),
-           "dckv_cache_append")
+    a = _AppendArgs(k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], qp, op, qs[0], qs[1], os_[0],
+                    os_[1], n, hq, 0, pos)
+    r = lib().dckv_cache_append(pool.ref, batch.ref, None if rope is None else ctypes.byref(rope), ctypes.byref(a), st,
+                                _device_stream(dev, stream))
+    if r:
+        _check(r, "dckv_cache_append")
 
 
 def dckv_cache_rows(pool, batch, rows, status, rope=None, positions=None, stream=None):
     """The sequences' first slots as rows [n, layers * 2 * heads * dim], keys rotated back by
     `rope` if given."""
-    if rows.dim() != 2 or rows.shape[1] != 2 * pool.n_layers * pool.n_kv_heads * pool.head_dim:
+    L, H, dim = pool.kv_shape
+    if rows.dim() != 2 or rows.shape[1] != 2 * L * H * dim:
         _bad("rows must be [n, layers * 2 * heads * dim]")
-    if _dtype_code(rows) != pool.dtype:
+    if _dtype_code(rows) != pool.code:
         _bad("rows must have the pool's type")
-    _pool_check(pool, batch, status, rows=rows, positions=positions)
+    st = _same_device(pool, batch, status)
+    rs = _on(pool.dev, "rows", rows)
+    n, pos = rows.shape[0], None
     if positions is not None:
-        _int32_check(positions=positions)
-        if positions.shape != rows.shape[:1]:
+        if positions.shape != (n,):
             _bad("positions must be [n]")
-    if rows.shape[0] == 0:
+        pos = _int32_on(pool.dev, "positions", positions)
+    if n == 0:
         return rows
-    _check(lib().dckv_cache_rows(ctypes.byref(pool), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
-                                 rows.data_ptr(), rows.stride(0), rows.shape[0], _ptr(positions), status.data_ptr(),
-                                 _device_stream(pool.device, stream)), "dckv_cache_rows")
+    r = lib().dckv_cache_rows(pool.ref, batch.ref, None if rope is None else ctypes.byref(rope), rows.data_ptr(), rs[0],
+                              n, pos, st, _device_stream(pool.dev, stream))
+    if r:
+        _check(r, "dckv_cache_rows")
     return rows
 
 
 def dckv_attention_workspace_bytes(pool, batch, n_q_heads) -> int:
-    n = int(lib().dckv_attention_workspace_bytes(ctypes.byref(pool), ctypes.byref(batch), int(n_q_heads)))
+    n = int(lib().dckv_attention_workspace_bytes(pool.ref, batch.ref, int(n_q_heads)))
     if n == 0:
         _bad(f"dckv_attention_workspace_bytes ({last_error()})")
     return n
@@ -558,23 +597,29 @@ def dckv_attention_workspace_bytes(pool, batch, n_q_heads) -> int:
 def dckv_attention(pool, layer, batch, q, out, status, workspace, scale=None, causal=True, lse=None, stream=None):
     """Attention of q [n, q heads, dim] over the sequences' slots in `layer` into out (same shape)
     and, if given, lse fp32 [n, q heads].  scale: dim ** -0.5 unless given."""
-    if q.dim() != 3 or q.shape[2] != pool.head_dim or out.shape != q.shape:
+    shape, dev = q.shape, pool.dev
+    if len(shape) != 3 or shape[2] != pool.dim or out.shape != shape:
         _bad("q and out must be [n, q heads, dim]")
-    if _dtype_code(q) != pool.dtype or out.dtype != q.dtype:
+    if _dtype_code(q) != pool.code or out.dtype != q.dtype:
         _bad("q and out must have the pool's type")
-    _pool_check(pool, batch, status, q=q, out=out, lse=lse, workspace=workspace)
-    n = q.shape[0]
-    a = _AttentionArgs(q.data_ptr(), out.data_ptr(), None, *q.stride()[:2], *out.stride()[:2], n, q.shape[1],
-                       int(layer), 1 if causal else 0, pool.head_dim ** -0.5 if scale is None else float(scale))
+    st = _same_device(pool, batch, status)
+    qs, os_ = _on(dev, "q", q), _on(dev, "out", out)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _bad("the workspace must be contiguous, on the pool's device")
+    lp = None
     if lse is not None:
-        if lse.shape != q.shape[:2] or _dtype_code(lse) != DCKV_FP32 or not lse.is_contiguous():
-            _bad("lse must be contiguous fp32 [n, q heads]")
-        a.lse = lse.data_ptr()
+        if lse.shape != shape[:2] or _dtype_code(lse) != DCKV_FP32 or lse.get_device() != dev or not lse.is_contiguous():
+            _bad("lse must be contiguous fp32 [n, q heads] on the pool's device")
+        lp = lse.data_ptr()
+    n = shape[0]
     if n == 0:
         return out
-    _check(lib().dckv_attention(ctypes.byref(pool), ctypes.byref(batch), ctypes.byref(a), status.data_ptr(),
-                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                _device_stream(pool.device, stream)), "dckv_attention")
+    a = _AttentionArgs(q.data_ptr(), out.data_ptr(), lp, qs[0], qs[1], os_[0], os_[1], n, shape[1], layer,
+                       1 if causal else 0, pool.dim ** -0.5 if scale is None else scale)
+    r = lib().dckv_attention(pool.ref, batch.ref, ctypes.byref(a), st, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _device_stream(dev, stream))
+    if r:
+        _check(r, "dckv_attention")
     return out
 
 

@@ -1011,71 +1011,90 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 
 // ------------------------------------------------------------------ joining split units
 // Block (c, y): if a unit begins in worker c's piece and is split, joins its rows y, y + gridDim.y, ...
-// Parts: slot 2 c + 1 (the beginning), then slot 2 i of the workers i up to the last.  Four
-// groups of threads take every fourth part, then add up.
-constexpr int JOIN_THREADS = 256;
+// Parts: slot 2 c + 1 (the beginning), then slot 2 i of the workers i up to the last.  With few
+// parts (many rows) each of the eight warps joins a row by itself; with more than
+// JOIN_WARP_PARTS the warps share a row, every eighth part each, and add up in shared memory: one
+// warp alone would wait for the parts one load latency after the other.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_THREADS = 32 * JOIN_WARPS;
+constexpr int JOIN_WARP_PARTS = 6;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const BatchDev bt, const AttnDev a, const AttnShape sh) {
-  constexpr int PER_ROW = D / 4;
-  constexpr int GROUPS = JOIN_THREADS / PER_ROW;
-  __shared__ float4 acc_sm[GROUPS][PER_ROW];
-  __shared__ float sum_sm[GROUPS];
-  const int c = blockIdx.x;
+  constexpr int E = D / 32;  // dims per lane, in vectors of V
+  constexpr int V = E >= 4 ? 4 : E;
+  __shared__ float acc_sm[JOIN_WARPS][D];
+  __shared__ float sum_sm[JOIN_WARPS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are still written
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 ds = a.desc[c];
   if (ds.x < 0) return;
+  const int parts = ds.z - c + 1;
+  const bool shared_row = parts > JOIN_WARP_PARTS;
+  const int step = shared_row ? JOIN_WARPS : 1, first = shared_row ? warp : 0;
   AttnWalk w;
   w.head = ds.y;
   w.unit = ds.x;
   w.t0 = 0;
   w.left = 1;
   walk_load(w, bt, a, sh);
-  const int grp = threadIdx.x / PER_ROW, d4 = threadIdx.x % PER_ROW;
-  const int parts = ds.z - c + 1;
-  for (int r = blockIdx.y; r < ds.w; r += gridDim.y) {
+  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)); };
+  for (int r = blockIdx.y + (shared_row ? 0 : warp * gridDim.y); r < ds.w; r += gridDim.y * (shared_row ? 1 : JOIN_WARPS)) {
+    // the parts' maxima and sums, one lane each
     float top = -INFINITY;
-    for (int i = 0; i < parts; ++i) {
-      const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
-      top = fmaxf(top, a.part_ml[slot * sh.rows + r].x);
-    }
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[slot_of(i) * sh.rows + r].x);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int i = grp; i < parts; i += GROUPS) {
-      const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
-      const float2 ml = a.part_ml[slot * sh.rows + r];
+    for (int i = first; i < parts; i += step) {
+      const int64_t at = slot_of(i) * sh.rows + r;
+      const float2 ml = a.part_ml[at];
       const float f = exp2_fast(ml.x - ref);
-      const float4 v = *reinterpret_cast<const float4 *>(a.part_o + ((int64_t)slot * sh.rows + r) * D + d4 * 4);
       sum = fmaf(f, ml.y, sum);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
-    }
-    acc_sm[grp][d4] = acc;
-    if (d4 == 0) sum_sm[grp] = sum;
-    __syncthreads();
-    if (grp == 0) {
-      for (int g = 1; g < GROUPS; ++g) {
-        const float4 v = acc_sm[g][d4];
-        sum += sum_sm[g];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      int64_t tok;
-      int head, sn;
-      if (unit_row(w, a, sh.rows, r, tok, head, sn)) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        store4<T>(reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh + d4 * 4,
-                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (a.lse && d4 == 0)
-          a.lse[tok * a.heads + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+      for (int v = 0; v < E / V; ++v) {
+        const Vec<float, V> x = *reinterpret_cast<const Vec<float, V> *>(a.part_o + at * D + (v * 32 + lane) * V);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[v * V + e] = fmaf(f, x.e[e], acc[v * V + e]);
       }
     }
-    __syncthreads();
+    if (shared_row) {
+#pragma unroll
+      for (int v = 0; v < E / V; ++v)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc_sm[warp][(v * 32 + lane) * V + e] = acc[v * V + e];
+      if (lane == 0) sum_sm[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int x = 1; x < JOIN_WARPS; ++x) {
+          sum += sum_sm[x];
+#pragma unroll
+          for (int v = 0; v < E / V; ++v)
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[v * V + e] += acc_sm[x][(v * 32 + lane) * V + e];
+        }
+      }
+    }
+    int64_t tok;
+    int head, sn;
+    if ((!shared_row || warp == 0) && unit_row(w, a, sh.rows, r, tok, head, sn)) {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      T *out = reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh;
+#pragma unroll
+      for (int v = 0; v < E / V; ++v) {
+        Vec<T, V> y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) y.e[e] = from_f<T>(acc[v * V + e] * inv);
+        *reinterpret_cast<Vec<T, V> *>(out + (v * 32 + lane) * V) = y;
+      }
+      if (a.lse && lane == 0)
+        a.lse[tok * a.heads + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+    if (shared_row) __syncthreads();
   }
 }
 
@@ -1143,38 +1162,61 @@ static int sm_count(int device, int &n) {
   return DCKV_OK;
 }
 
+// Allows a kernel its dynamic shared memory, once per device.
+static int allow_smem(const void *kern, int smem, int device, std::atomic<uint64_t> &done) {
+  if (done.load() >> device & 1) return DCKV_OK;
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  done.fetch_or(1ull << device);
+  return DCKV_OK;
+}
+
+// The join is launched with programmatic stream serialisation: its blocks are set up while the
+// first kernel ends and wait for its memory (griddepcontrol.wait).
+template <typename T, int D>
+static int run_join(const BatchDev &b, const AttnDev &a, const AttnShape &sh, int row_blocks, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.workers, (unsigned)row_blocks);
+  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  CK(cudaLaunchKernelEx(&cfg, k_attend_join<T, D>, b, a, sh));
+  ++g_launches;
+  return DCKV_OK;
+}
+
 template <typename T, int D, int NT>
 static int run_attend_few(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
-                          const AttnDev &a, const AttnShape &sh, cudaStream_t st) {
+                          const AttnDev &a, const AttnShape &sh, int device, cudaStream_t st) {
   auto kern = k_attend_few<T, D, NT>;
-  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeAttn<D, NT>::SMEM));
+  static std::atomic<uint64_t> allowed{0};
+  RET(allow_smem((const void *)kern, DecodeAttn<D, NT>::SMEM, device, allowed));
   kern<<<a.workers, DEC_ATTN_THREADS, DecodeAttn<D, NT>::SMEM, st>>>(mk, mv, p, b, a, sh);
   ++g_launches;
-  k_attend_join<T, D><<<dim3(a.workers, 8), JOIN_THREADS, 0, st>>>(b, a, sh);
-  ++g_launches;
   CK(cudaGetLastError());
-  return DCKV_OK;
+  return run_join<T, D>(b, a, sh, 8, st);
 }
 
 template <typename T, int D>
 static int run_attend_many(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
-                           const AttnDev &a, const AttnShape &sh, const PairMaps &mp, cudaStream_t st) {
+                           const AttnDev &a, const AttnShape &sh, const PairMaps &mp, int device, cudaStream_t st) {
   auto kern = k_attend_many<T, D>;
-  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairAttn<D>::SMEM));
+  static std::atomic<uint64_t> allowed{0};
+  RET(allow_smem((const void *)kern, PairAttn<D>::SMEM, device, allowed));
   void *args[] = {(void *)&mk, (void *)&mv, (void *)&p, (void *)&b, (void *)&a, (void *)&sh, (void *)&mp};
   RET(launch_pairs((const void *)kern, a.workers, 2 * a.workers, PAIR_THREADS, PairAttn<D>::SMEM, st, args));
-  k_attend_join<T, D><<<dim3(a.workers, 32), JOIN_THREADS, 0, st>>>(b, a, sh);
-  ++g_launches;
-  CK(cudaGetLastError());
-  return DCKV_OK;
+  return run_join<T, D>(b, a, sh, 32, st);
 }
 
 template <typename T, int D>
 static int run_attend(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
-                      const AttnDev &a, const AttnShape &sh, const PairMaps &mp, cudaStream_t st) {
-  if (sh.rows == 8) return run_attend_few<T, D, 1>(mk, mv, p, b, a, sh, st);
-  if (sh.rows == 16) return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, st);
-  return run_attend_many<T, D>(mk, mv, p, b, a, sh, mp, st);
+                      const AttnDev &a, const AttnShape &sh, const PairMaps &mp, int device, cudaStream_t st) {
+  if (sh.rows == 8) return run_attend_few<T, D, 1>(mk, mv, p, b, a, sh, device, st);
+  if (sh.rows == 16) return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, device, st);
+  return run_attend_many<T, D>(mk, mv, p, b, a, sh, mp, device, st);
 }
 
 // Rows of a TMA box: the largest power of two up to `most` that divides a page, so that no box
@@ -1239,11 +1281,11 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   RET(map_pages(&mk, p.k + 2 * args->layer * p.kl, bf, p, p.kr, p.kh, p.kp, mp.k_box));
   RET(map_pages(&mv, p.v + 2 * args->layer * p.vl, bf, p, p.vr, p.vh, p.vp, mp.v_box, many && p.dim == 64 ? 32 : 64));
   if (p.dim == 64)
-    return bf ? run_attend<__nv_bfloat16, 64>(mk, mv, p, b, a, sh, mp, st)
-              : run_attend<__half, 64>(mk, mv, p, b, a, sh, mp, st);
+    return bf ? run_attend<__nv_bfloat16, 64>(mk, mv, p, b, a, sh, mp, pool->device, st)
+              : run_attend<__half, 64>(mk, mv, p, b, a, sh, mp, pool->device, st);
   if (p.dim == 128)
-    return bf ? run_attend<__nv_bfloat16, 128>(mk, mv, p, b, a, sh, mp, st)
-              : run_attend<__half, 128>(mk, mv, p, b, a, sh, mp, st);
-  return bf ? run_attend<__nv_bfloat16, 256>(mk, mv, p, b, a, sh, mp, st)
-            : run_attend<__half, 256>(mk, mv, p, b, a, sh, mp, st);
+    return bf ? run_attend<__nv_bfloat16, 128>(mk, mv, p, b, a, sh, mp, pool->device, st)
+              : run_attend<__half, 128>(mk, mv, p, b, a, sh, mp, pool->device, st);
+  return bf ? run_attend<__nv_bfloat16, 256>(mk, mv, p, b, a, sh, mp, pool->device, st)
+            : run_attend<__half, 256>(mk, mv, p, b, a, sh, mp, pool->device, st);
 }

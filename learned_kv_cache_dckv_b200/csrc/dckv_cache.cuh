@@ -394,9 +394,15 @@ extern "C" int dckv_rope_init(dckv_rope_spec *out, int rotary_dim, int layout, d
   return DCKV_OK;
 }
 
-extern "C" int dckv_rope(const dckv_rope_spec *spec, int mode, int device, int dtype, const void *x, int64_t x_token_stride,
-                         int64_t x_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride,
-                         int64_t n_tokens, int n_heads, int head_dim, const int32_t *positions, void *stream) {
+extern "C" int dckv_rope(const dckv_rope_spec *spec, int mode, const dckv_rope_args *args, void *stream) {
+  if (!args) return fail(DCKV_EINVAL, "a pointer argument is NULL");
+  const void *x = args->x;
+  void *out = args->out;
+  const int32_t *positions = args->positions;
+  int64_t x_token_stride = args->x_token_stride, x_head_stride = args->x_head_stride;
+  int64_t out_token_stride = args->out_token_stride, out_head_stride = args->out_head_stride;
+  const int64_t n_tokens = args->n_tokens;
+  const int n_heads = args->n_heads, head_dim = args->head_dim, dtype = args->dtype, device = args->device;
   if (!spec || !x || !out || !positions) return fail(DCKV_EINVAL, "a pointer argument is NULL");
   RET(check_device(device));
   RopeDev rope;

@@ -53,8 +53,9 @@ def _rope(**kw):
              heads=2, dim=256, pos=FAKE)
     a.update(kw)
     spec = None if a["spec"] is None else ctypes.byref(a["spec"])
-    return D.lib().dckv_rope(spec, a["mode"], a["device"], a["dtype"], a["x"], a["xt"], a["xh"], a["out"], a["ot"],
-                             a["oh"], a["n"], a["heads"], a["dim"], a["pos"], None)
+    args = D._RopeArgs(a["x"], a["out"], a["xt"], a["xh"], a["ot"], a["oh"], a["n"], a["heads"], a["dim"], a["pos"],
+                       a["dtype"], a["device"])
+    return D.lib().dckv_rope(spec, a["mode"], ctypes.byref(args), None)
 
 
 @pytest.mark.parametrize("bad", [dict(spec=None), dict(x=None), dict(out=None), dict(pos=None), dict(mode=3),
