@@ -818,8 +818,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         const int n = w.t1 - w.t0;
         for (int t = 0; t < n && ok; ++t, ++tile) {
           if (t + 1 < n) scores(tile + 1);
-          if (ok && t == 0 && item > 0) ok = mbar_wait_cluster(&bars->o_empty, (item - 1) & 1u, abort_flag);
-          if (ok) ok = mbar_wait_cluster(&bars->p_full[tile & 1u], (tile >> 1) & 1u, abort_flag);
+          if (ok && t == 0 && item > 0) ok = mbar_wait(&bars->o_empty, (item - 1) & 1u, abort_flag);
+          if (ok) ok = mbar_wait(&bars->p_full[tile & 1u], (tile >> 1) & 1u, abort_flag);
           if (ok) ok = mbar_wait_cluster(&bars->full[stage], phase, abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_release(l_p[tile & 1u]);
+        if (lane == 0) mbar_arrive_cluster(l_p[tile & 1u]);  // TMEM only: ordered by the tcgen05 fences
       }
       // every S of this unit is computed, so Q may be replaced
       AttnWalk nw = w;
@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_release(l_o);
+      if (lane == 0) mbar_arrive_cluster(l_o);
       w = nw;
     } while (more);
   }
