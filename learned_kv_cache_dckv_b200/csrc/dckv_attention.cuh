@@ -27,6 +27,7 @@ struct AttnDev {
   float *lse;
   int64_t qt, qh, ot, oh;
   int heads, group, causal;
+  FastDiv group_div;
   float scale_log2;
   int32_t *status;
   float *part_o;   // [2 workers][rows][dim]
@@ -56,17 +57,18 @@ __device__ __forceinline__ int seen_slots(const SeqView &s, int t, int causal) {
   return causal ? max(0, s.len - s.n + t + 1) : s.len;
 }
 
-// Slots that row tile rt sees (its last row's), -1 where it has no rows.
-__device__ __forceinline__ int tile_seen(const SeqView &s, int rt, int rows, int group, int causal) {
-  const int64_t n_rows = (int64_t)s.n * group, r0 = (int64_t)rt * rows;
-  if (r0 >= n_rows) return -1;
-  const int64_t last = min(n_rows, r0 + rows) - 1;
-  return seen_slots(s, (int)(last / group), causal);
+// Slots that row tile rt sees (its last row's), -1 where it has no rows.  A sequence's packed
+// rows number below 2^31 (checked on the host).
+__device__ __forceinline__ int tile_seen(const SeqView &s, int rt, int rows, const AttnDev &a) {
+  const int n_rows = s.n * a.group;
+  if ((int64_t)rt * rows >= n_rows) return -1;
+  const int last = min(n_rows - rt * rows, rows) - 1 + rt * rows;
+  return seen_slots(s, a.group_div.div(last), a.causal);
 }
 
 // Key tiles of a unit; one that sees no slot still has one, to write its zeros.
 __device__ __forceinline__ int unit_tiles(int seen, int key_tile) {
-  return seen < 0 ? 0 : max(1, (int)(((int64_t)seen + key_tile - 1) / key_tile));
+  return seen < 0 ? 0 : max(1, (int)(((uint32_t)seen + key_tile - 1) / (uint32_t)key_tile));
 }
 
 // A block's walk along the line of tiles: the current unit and the tiles [t0, t1) of it that
@@ -81,15 +83,16 @@ struct AttnWalk {
 
 struct AttnShape {
   int rows, key_tile, row_tiles, units, kv_heads;
+  FastDiv unit_div;  // by row_tiles
   int64_t max_slots;
 };
 
 // Fills the walk's unit fields from (head, unit); t0 is given.
 __device__ __forceinline__ void walk_load(AttnWalk &w, const BatchDev &bt, const AttnDev &a, const AttnShape &sh) {
-  w.b = w.unit / sh.row_tiles;
+  w.b = sh.unit_div.div(w.unit);
   w.rt = w.unit - w.b * sh.row_tiles;
   load_seq(bt, sh.max_slots, w.b, w.s);
-  w.seen = tile_seen(w.s, w.rt, sh.rows, a.group, a.causal);
+  w.seen = tile_seen(w.s, w.rt, sh.rows, a);
   w.tiles = unit_tiles(w.seen, sh.key_tile);
   w.t1 = (int)min((int64_t)w.tiles, w.t0 + w.left);
 }
@@ -121,12 +124,20 @@ struct AttnPlan {
   int workers;    // blocks that take a piece
 };
 
+// a / b in 32 bits where both fit (64-bit division is a long subroutine).
+__device__ __forceinline__ int64_t div_wide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // First tile of worker c's piece.
-__device__ __forceinline__ int64_t piece_start(const AttnPlan &pl, int c) { return (int64_t)c * pl.line / pl.workers; }
+__device__ __forceinline__ int64_t piece_start(const AttnPlan &pl, int c) {
+  return div_wide((int64_t)c * pl.line, pl.workers);
+}
 
 // Worker whose piece holds tile p of the line.
 __device__ __forceinline__ int piece_of(const AttnPlan &pl, int64_t p) {
-  return (int)(((p + 1) * pl.workers + pl.line - 1) / pl.line) - 1;
+  return (int)div_wide((p + 1) * pl.workers + pl.line - 1, pl.line) - 1;
 }
 
 // Counts every unit's tiles (each thread a run of units, then a block scan), and finds worker
@@ -142,13 +153,13 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
   int b = -1;
   SeqView s;
   for (int u = u0; u < u1; ++u) {
-    const int bu = u / sh.row_tiles;
+    const int bu = sh.unit_div.div(u);
     if (bu != b) {
       b = bu;
       const bool ok = load_seq(bt, sh.max_slots, b, s);
       if (!ok && c == 0) atomicExch(a.status, DCKV_ERANGE);
     }
-    mine += unit_tiles(tile_seen(s, u - b * sh.row_tiles, sh.rows, a.group, a.causal), sh.key_tile);
+    mine += unit_tiles(tile_seen(s, u - b * sh.row_tiles, sh.rows, a), sh.key_tile);
   }
   int64_t incl = mine;
   for (int o = 1; o < 32; o <<= 1) {
@@ -165,19 +176,19 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
   }
   pl.total = total;
   pl.line = total * sh.kv_heads;
-  pl.workers = (int)max((int64_t)1, min((int64_t)a.workers, pl.line / min_tiles));
+  pl.workers = (int)max((int64_t)1, min((int64_t)a.workers, div_wide(pl.line, min_tiles)));
   if (pl.line == 0 || c >= pl.workers) return false;
   const int64_t start = piece_start(pl, c);
   w.left = piece_start(pl, c + 1) - start;
-  w.head = (int)(start / total);
+  w.head = (int)div_wide(start, total);
   const int64_t pos = start - w.head * total;
   int64_t at = before + incl - mine;
   if (pos >= at && pos < at + mine) {  // the start lies in this thread's run: walk it
     int u = u0;
     for (; u < u1; ++u) {
-      const int bu = u / sh.row_tiles;
+      const int bu = sh.unit_div.div(u);
       load_seq(bt, sh.max_slots, bu, s);
-      const int t = unit_tiles(tile_seen(s, u - bu * sh.row_tiles, sh.rows, a.group, a.causal), sh.key_tile);
+      const int t = unit_tiles(tile_seen(s, u - bu * sh.row_tiles, sh.rows, a), sh.key_tile);
       if (pos < at + t) break;
       at += t;
     }
@@ -249,11 +260,11 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
 // Where a unit's row r goes: token and query head; false past its last row.
 __device__ __forceinline__ bool unit_row(const AttnWalk &w, const AttnDev &a, int rows, int r, int64_t &tok, int &head,
                                          int &seen) {
-  const int64_t i = (int64_t)w.rt * rows + r;
-  if (i >= (int64_t)w.s.n * a.group) return false;
-  const int t = (int)(i / a.group);
+  const int i = w.rt * rows + r;
+  if (i >= w.s.n * a.group) return false;
+  const int t = a.group_div.div(i);
   tok = w.s.first + t;
-  head = w.head * a.group + (int)(i - (int64_t)t * a.group);
+  head = w.head * a.group + i - t * a.group;
   seen = seen_slots(w.s, t, a.causal);
   return true;
 }
@@ -344,7 +355,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
       const int key = slice_key(pt++);
       if (key >= pw.seen) continue;
       if (lane == 0) {
-        const int pi = key / p.page_size;
+        const int pi = p.page_div.div(key);
         int page = __ldg(bt.page_table + pw.b * bt.table_stride + pi);
         if (page < 0 || page >= p.n_pages) {  // past the pool: the copy fills zeros
           atomicExch(a.status, DCKV_ERANGE);
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
     const int slot = begins ? 2 * c + 1 : 2 * c;
     if (begins && !ends && threadIdx.x == 0) {
       const int64_t line_end = piece_start(pl, c + 1) - w.left + w.tiles;  // behind the unit's last tile (t0 = 0)
-      const int rows = (int)min((int64_t)C::ROWS, (int64_t)w.s.n * a.group - (int64_t)w.rt * C::ROWS);
+      const int rows = min(C::ROWS, w.s.n * a.group - w.rt * C::ROWS);
       a.desc[c] = make_int4(w.unit, w.head, piece_of(pl, line_end - 1), rows);
     }
     constexpr int PER_ROW = D / 4;
@@ -717,7 +728,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       const int key = key0 + g * box;
       int page = (int)p.n_pages, row = 0;  // behind the pool: the copy fills zeros
       if (blk < blocks && key < wk.s.len) {
-        const int pi = key / p.page_size;
+        const int pi = p.page_div.div(key);
         row = key - pi * p.page_size;
         page = __ldg(bt.page_table + wk.b * bt.table_stride + pi);
         if (page < 0 || page >= p.n_pages) {
@@ -728,8 +739,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       }
       // a V box that the sequence's last slot ends in: the rows behind it may hold anything, and
       // 0 * NaN is NaN, so they are cleared before the MMA sees them
-      const int last_box = wk.s.len / box * box;  // first key of the box that holds slot `len`
-      const bool ragged = is_v && wk.s.len % box != 0 && last_box >= key0 && last_box < key0 + PAIR_KEYS;
+      const int last_box = wk.s.len & ~(box - 1);  // first key of the box that holds slot `len`
+      const bool ragged = is_v && last_box != wk.s.len && last_box >= key0 && last_box < key0 + PAIR_KEYS;
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag));
       if (!ok) return;
       uint8_t *dst = bufs + stage * C::BUF_BYTES;
@@ -992,7 +1003,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       }
       if (begins && !ends && rank == 0 && sw == 0 && lane == 0) {
         const int64_t line_end = piece_start(pl, c + 1) - w.left + w.tiles;
-        const int rows = (int)min((int64_t)PAIR_ROWS, (int64_t)w.s.n * a.group - (int64_t)w.rt * PAIR_ROWS);
+        const int rows = min(PAIR_ROWS, w.s.n * a.group - w.rt * PAIR_ROWS);
         a.desc[c] = make_int4(w.unit, w.head, piece_of(pl, line_end - 1), rows);
       }
       tc_fence_before();
@@ -1258,9 +1269,12 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   const bool many = sh.rows == PAIR_ROWS;
   sh.key_tile = many ? PAIR_KEYS : DEC_KEY_TILE;
   sh.kv_heads = p.heads;
-  const int64_t row_tiles = ((int64_t)std::min<int64_t>(b.max_new, std::max<int64_t>(n, 1)) * group + sh.rows - 1) / sh.rows;
+  const int64_t most_rows = std::min<int64_t>(b.max_new, std::max<int64_t>(n, 1)) * group;
+  if (most_rows > 0x7fffffffll - PAIR_ROWS) return fail(DCKV_EINVAL, "max_new times the head group is too large");
+  const int64_t row_tiles = (most_rows + sh.rows - 1) / sh.rows;
   if (row_tiles * b.batch > 0x7fffffffll) return fail(DCKV_EINVAL, "batch times max_new is too large");
   sh.row_tiles = (int)row_tiles;
+  sh.unit_div = FastDiv((uint32_t)row_tiles);
   sh.units = (int)(row_tiles * b.batch);
   sh.max_slots = std::min<int64_t>((int64_t)b.max_pages * p.page_size, 0x7fffffffll - 65536);
   const AttnLayout lay = attn_layout(sh.rows, p.dim);
@@ -1272,7 +1286,7 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   RET(sm_count(pool->device, sms));
   char *ws = (char *)workspace;
   const AttnDev a{(const char *)args->q, (char *)args->out, args->lse, qt, qh, ot, oh, hq, group, args->causal,
-                  args->scale * 1.4426950408889634f, status, (float *)(ws + lay.part_o), (float2 *)(ws + lay.part_ml),
+                  FastDiv((uint32_t)group), args->scale * 1.4426950408889634f, status, (float *)(ws + lay.part_o), (float2 *)(ws + lay.part_ml),
                   (int4 *)(ws + lay.desc),
                   many ? std::min(sms / 2, ATTN_MAX_PAIRS) : std::min(sms, ATTN_MAX_WORKERS)};
   const bool bf = pool->dtype == DCKV_BF16;

@@ -27,9 +27,27 @@ struct RopeDev {
   double freq[DCKV_ROPE_MAX_PAIRS] = {};
 };
 
+// Division of n < 2^31 by a divisor known on the host, as a multiplication: with s = ceil(log2 d)
+// and m = ceil(2^(31 + s) / d), n m exceeds n 2^(31 + s) / d by less than 2^(31 + s) / d.  (A
+// hardware division is some 30 dependent instructions in 32 bits and a subroutine in 64; these
+// kernels divide in their set-up, where every instruction is latency.)
+struct FastDiv {
+  uint32_t d = 1, m = 1u << 31;
+  int s = 31;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    int l = 0;
+    while ((1ull << l) < div) ++l;
+    s = 31 + l;
+    m = (uint32_t)(((1ull << s) + div - 1) / div);
+  }
+  __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> s); }
+};
+
 struct PoolDev {
   char *k, *v;
   int n_layers, heads, dim, page_size;
+  FastDiv page_div;
   int64_t n_pages;
   int64_t kl, kp, kr, kh, vl, vp, vr, vh;  // element strides: layer, page, row, head
 };
@@ -171,11 +189,13 @@ __device__ __forceinline__ int find_sequence(const BatchDev &bt, int64_t t, int 
   return t >= __ldg(bt.offsets + lo) && t < __ldg(bt.offsets + lo + 1) ? lo : -1;
 }
 
-// Page of slot j of sequence b, or -1 where the table or the pool ends before it.
+// Page of slot j (below 2^31) of sequence b, or -1 where the table or the pool ends before it.
 __device__ __forceinline__ int64_t slot_page(const PoolDev &p, const BatchDev &bt, int b, int64_t j, int &row) {
-  const int64_t pi = j / p.page_size;
-  row = (int)(j - pi * p.page_size);
-  if (j < 0 || pi >= bt.max_pages) return -1;
+  row = 0;
+  if (j < 0) return -1;
+  const int pi = p.page_div.div((int)j);
+  row = (int)j - pi * p.page_size;
+  if (pi >= bt.max_pages) return -1;
   const int page = __ldg(bt.page_table + b * bt.table_stride + pi);
   return page >= 0 && page < p.n_pages ? page : -1;
 }
@@ -329,7 +349,7 @@ static int check_pool(const dckv_kv_pool *p, PoolDev &d) {
       bad_stride(p->k_head_stride, p->n_kv_heads, 8) || bad_stride(p->v_head_stride, p->n_kv_heads, 8))
     return fail(DCKV_EINVAL, "pool strides must be positive multiples of 8 elements");
   d = PoolDev{(char *)p->k,       (char *)p->v,       p->n_layers,     p->n_kv_heads,   p->head_dim,
-              p->page_size,       p->n_pages,         p->k_layer_stride, p->k_page_stride, p->k_row_stride,
+              p->page_size,       FastDiv((uint32_t)p->page_size), p->n_pages,         p->k_layer_stride, p->k_page_stride, p->k_row_stride,
               p->k_head_stride,   p->v_layer_stride,  p->v_page_stride, p->v_row_stride,  p->v_head_stride};
   return DCKV_OK;
 }
