@@ -32,7 +32,8 @@ struct AttnDev {
   int32_t *status;
   float *part_o;   // [2 workers][rows][dim]
   float2 *part_ml; // [2 workers][rows] (m, l)
-  int4 *desc;      // [workers] {unit, KV head, last worker, rows}: a unit begins here and is split
+  int4 *desc;      // [workers][2]: a split unit that begins here {last worker (-1: none), rows, first
+                   // token, first packed row}, {KV head, ...}
   int workers;
 };
 
@@ -112,16 +113,23 @@ __device__ __forceinline__ bool walk_next(AttnWalk &w, const BatchDev &bt, const
   return true;
 }
 
+// How the line is cut.  By default into equal pieces, wherever they begin and end (stream): no
+// block waits for another, but a block may pass from unit to unit, which costs it the time of
+// PLAN_STEPS tiles or so (the old unit's join or output, the new unit's Q).  Where every unit can
+// be cut into equal parts of at most T tiles, one part per block, with T no more than that above
+// the stream's piece, the parts win (parts).
+constexpr int PLAN_TRIES = 4;
+
 struct AttnPlanSmem {
   int64_t warp_sum[32];
-  int64_t total;
+  int warp_cnt[32][PLAN_TRIES];
   int unit, off;
 };
 
 struct AttnPlan {
-  int64_t total;  // tiles of one head's units
-  int64_t line;   // tiles of all heads
-  int workers;    // blocks that take a piece
+  int64_t line;  // tiles of all units and heads
+  int workers;   // blocks that take a piece
+  int part;      // most tiles of a part; 0: stream
 };
 
 // a / b in 32 bits where both fit (64-bit division is a long subroutine).
@@ -130,21 +138,24 @@ __device__ __forceinline__ int64_t div_wide(int64_t a, int64_t b) {
   return a / b;
 }
 
-// First tile of worker c's piece.
+// First tile of worker c's piece (stream).
 __device__ __forceinline__ int64_t piece_start(const AttnPlan &pl, int c) {
   return div_wide((int64_t)c * pl.line, pl.workers);
 }
 
-// Worker whose piece holds tile p of the line.
-__device__ __forceinline__ int piece_of(const AttnPlan &pl, int64_t p) {
-  return (int)div_wide((p + 1) * pl.workers + pl.line - 1, pl.line) - 1;
+// Last worker of the unit that begins in worker c's piece (w.t0 = 0).
+__device__ __forceinline__ int last_worker(const AttnPlan &pl, const AttnWalk &w, int c) {
+  if (pl.part) return c + (w.tiles + pl.part - 1) / pl.part - 1;
+  const int64_t end = piece_start(pl, c + 1) - w.left + w.tiles;  // behind the unit's last tile
+  return (int)div_wide(end * pl.workers + pl.line - 1, pl.line) - 1;
 }
 
-// Counts every unit's tiles (each thread a run of units, then a block scan), and finds worker
-// c's start.  Called by all threads of the block; returns false where c has no piece.
+// Counts every unit's tiles (each thread a run of units, then a block scan), chooses the cut and
+// finds worker c's start.  Called by all threads of the block; returns false where c has no piece.
+// tries: cuts into parts to look at (1 .. PLAN_TRIES), part sizes from the stream's piece upwards.
 template <int THREADS>
-__device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, const AttnShape &sh, int min_tiles,
-                                          int c, AttnPlanSmem *sm, AttnPlan &pl, AttnWalk &w) {
+__device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, const AttnShape &sh, int tries, int c,
+                                          AttnPlanSmem *sm, AttnPlan &pl, AttnWalk &w) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (sh.units + THREADS - 1) / THREADS;
@@ -152,15 +163,17 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
   int64_t mine = 0;
   int b = -1;
   SeqView s;
-  for (int u = u0; u < u1; ++u) {
+  auto tiles_of = [&](int u) {
     const int bu = sh.unit_div.div(u);
     if (bu != b) {
       b = bu;
       const bool ok = load_seq(bt, sh.max_slots, b, s);
       if (!ok && c == 0) atomicExch(a.status, DCKV_ERANGE);
     }
-    mine += unit_tiles(tile_seen(s, u - b * sh.row_tiles, sh.rows, a), sh.key_tile);
-  }
+    return unit_tiles(tile_seen(s, u - b * sh.row_tiles, sh.rows, a), sh.key_tile);
+  };
+  int one = 0;  // the thread's tiles if it has a single unit
+  for (int u = u0; u < u1; ++u) mine += one = tiles_of(u);
   int64_t incl = mine;
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -174,10 +187,73 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
     if (i < warp) before += v;
     total += v;
   }
-  pl.total = total;
   pl.line = total * sh.kv_heads;
-  pl.workers = (int)max((int64_t)1, min((int64_t)a.workers, div_wide(pl.line, min_tiles)));
-  if (pl.line == 0 || c >= pl.workers) return false;
+  pl.workers = (int)max((int64_t)1, min((int64_t)a.workers, pl.line));
+  pl.part = 0;
+  if (pl.line == 0) return false;
+  // parts: sizes base, base + step, ...
+  const int64_t base = div_wide(pl.line + pl.workers - 1, pl.workers);
+  const int step = (int)max((int64_t)1, min(base >> 5, (int64_t)1 << 20));
+  int cnt[PLAN_TRIES], scan[PLAN_TRIES], pieces = 0, pieces_before = 0;
+  if (sh.units <= a.workers && base < (1 << 24)) {
+#pragma unroll
+    for (int j = 0; j < PLAN_TRIES; ++j) cnt[j] = 0;
+    for (int u = u0; u < u1; ++u) {
+      const int t = per == 1 ? one : tiles_of(u);
+#pragma unroll
+      for (int j = 0; j < PLAN_TRIES; ++j) cnt[j] += (int)((uint32_t)(t + (int)base + j * step - 1) / (uint32_t)((int)base + j * step));
+    }
+#pragma unroll
+    for (int j = 0; j < PLAN_TRIES; ++j) {
+      scan[j] = cnt[j];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, scan[j], o);
+        if (lane >= o) scan[j] += v;
+      }
+      if (lane == 31) sm->warp_cnt[warp][j] = scan[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PLAN_TRIES; ++j) {
+      int sum = 0, bef = 0;
+      for (int i = 0; i < WARPS; ++i) {
+        const int v = sm->warp_cnt[i][j];
+        if (i < warp) bef += v;
+        sum += v;
+      }
+      if (j < tries && pl.part == 0 && (int64_t)sum * sh.kv_heads <= a.workers) {
+        pl.part = (int)base + j * step;
+        pieces = sum;
+        pieces_before = bef + scan[j] - cnt[j];
+      }
+    }
+  }
+  if (pl.part) {
+    pl.workers = pieces * sh.kv_heads;
+    if (c >= pl.workers) return false;
+    w.head = c / pieces;
+    const int pos = c - w.head * pieces;
+    int at = pieces_before;
+    for (int u = u0; u < u1; ++u) {  // the unit of this worker, in one thread's run
+      const int n = (tiles_of(u) + pl.part - 1) / pl.part;
+      if (pos >= at && pos < at + n) {
+        sm->unit = u;
+        sm->off = pos - at;
+      }
+      at += n;
+    }
+    __syncthreads();
+    w.unit = sm->unit;
+    w.t0 = 0;
+    w.left = 0x7fffffff;
+    walk_load(w, bt, a, sh);
+    const int n = (w.tiles + pl.part - 1) / pl.part, k = sm->off;
+    w.t0 = (int)((int64_t)w.tiles * k / n);
+    w.t1 = (int)((int64_t)w.tiles * (k + 1) / n);
+    w.left = w.t1 - w.t0;
+    return true;
+  }
+  if (c >= pl.workers) return false;
   const int64_t start = piece_start(pl, c);
   w.left = piece_start(pl, c + 1) - start;
   w.head = (int)div_wide(start, total);
@@ -186,9 +262,7 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
   if (pos >= at && pos < at + mine) {  // the start lies in this thread's run: walk it
     int u = u0;
     for (; u < u1; ++u) {
-      const int bu = sh.unit_div.div(u);
-      load_seq(bt, sh.max_slots, bu, s);
-      const int t = unit_tiles(tile_seen(s, u - bu * sh.row_tiles, sh.rows, a), sh.key_tile);
+      const int t = tiles_of(u);
       if (pos < at + t) break;
       at += t;
     }
@@ -269,6 +343,12 @@ __device__ __forceinline__ bool unit_row(const AttnWalk &w, const AttnDev &a, in
   return true;
 }
 
+// The join's description of a split unit that begins in worker c's piece.
+__device__ __forceinline__ void describe(const AttnDev &a, const AttnPlan &pl, const AttnWalk &w, int c, int rows) {
+  a.desc[2 * c + 1] = make_int4(w.head, 0, 0, 0);
+  a.desc[2 * c] = make_int4(last_worker(pl, w, c), min(rows, w.s.n * a.group - w.rt * rows), (int)w.s.first, w.rt * rows);
+}
+
 template <typename T>
 __device__ __forceinline__ void store4(T *dst, float4 v) {
   uint2 p = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
@@ -330,11 +410,12 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
     }
     fence_mbar_init();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   AttnPlan pl;
   AttnWalk w;
   const int c = blockIdx.x;
-  const bool any = attn_plan<DEC_ATTN_THREADS>(bt, a, sh, 1, c, &plan_sm, pl, w);
-  if (threadIdx.x == 0) a.desc[c] = make_int4(-1, 0, 0, 0);
+  const bool any = attn_plan<DEC_ATTN_THREADS>(bt, a, sh, 2, c, &plan_sm, pl, w);
+  if (threadIdx.x == 0) a.desc[2 * c] = make_int4(-1, 0, 0, 0);
   if (!any) return;
   __syncwarp();
 
@@ -541,11 +622,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
     __syncthreads();
     const bool begins = w.t0 == 0, ends = w.t1 == w.tiles;
     const int slot = begins ? 2 * c + 1 : 2 * c;
-    if (begins && !ends && threadIdx.x == 0) {
-      const int64_t line_end = piece_start(pl, c + 1) - w.left + w.tiles;  // behind the unit's last tile (t0 = 0)
-      const int rows = min(C::ROWS, w.s.n * a.group - w.rt * C::ROWS);
-      a.desc[c] = make_int4(w.unit, w.head, piece_of(pl, line_end - 1), rows);
-    }
+    if (begins && !ends && threadIdx.x == 0) describe(a, pl, w, c, C::ROWS);
     constexpr int PER_ROW = D / 4;
     for (int i = threadIdx.x; i < C::ROWS * PER_ROW; i += DEC_ATTN_THREADS) {
       const int r = i / PER_ROW, d = (i - r * PER_ROW) * 4;
@@ -623,7 +700,7 @@ struct PairAttn {
   static constexpr int BUF_BYTES = 64 * D * 2;  // half of K, or half of V
   static constexpr int V_ROW = D >= 128 ? 128 : 64;  // bytes of a V half's row in one block
   static constexpr int V_BLOCKS = D >= 128 ? D / 128 : 1;
-  static constexpr int AREA = 512 + 2048 + 512;  // barriers, exchange, plan
+  static constexpr int AREA = 512 + 2048;  // barriers; exchange, before that the plan
   static constexpr int FIT = (232448 - AREA - Q_BYTES) / BUF_BYTES;
   static constexpr int STAGES = FIT > 10 ? 10 : FIT;
   static constexpr int SMEM = Q_BYTES + STAGES * BUF_BYTES + AREA;
@@ -666,9 +743,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   uint8_t *q_sm = dyn_smem;
   uint8_t *bufs = dyn_smem + C::Q_BYTES;
   PairBars<STAGES> *bars = reinterpret_cast<PairBars<STAGES> *>(bufs + STAGES * C::BUF_BYTES);
-  static_assert(sizeof(PairBars<STAGES>) <= 512 && sizeof(AttnPlanSmem) <= 512, "barrier area");
+  static_assert(sizeof(PairBars<STAGES>) <= 512 && sizeof(AttnPlanSmem) <= 2048, "barrier area");
   float *xch = reinterpret_cast<float *>(bufs + STAGES * C::BUF_BYTES + 512);  // [tile parity][half][row]
-  AttnPlanSmem *plan_sm = reinterpret_cast<AttnPlanSmem *>(bufs + STAGES * C::BUF_BYTES + 512 + 2048);
+  AttnPlanSmem *plan_sm = reinterpret_cast<AttnPlanSmem *>(xch);
   GemmTail<STAGES> *tail = &bars->tail;
   volatile int *abort_flag = &tail->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -700,10 +777,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     tmem_alloc_pair(&tail->tmem_base, 512);
     tmem_relinquish_pair();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   AttnPlan pl;
   AttnWalk w;
-  const bool any = attn_plan<PAIR_THREADS>(bt, a, sh, 1, c, plan_sm, pl, w);
-  if (threadIdx.x == 0 && rank == 0) a.desc[c] = make_int4(-1, 0, 0, 0);
+  const bool any = attn_plan<PAIR_THREADS>(bt, a, sh, PLAN_TRIES, c, plan_sm, pl, w);
+  if (threadIdx.x == 0 && rank == 0) a.desc[2 * c] = make_int4(-1, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are initialised before any cross-CTA signal
@@ -1001,11 +1079,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           else if (a.lse) a.lse[tok * a.heads + head] = sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
         }
       }
-      if (begins && !ends && rank == 0 && sw == 0 && lane == 0) {
-        const int64_t line_end = piece_start(pl, c + 1) - w.left + w.tiles;
-        const int rows = min(PAIR_ROWS, w.s.n * a.group - w.rt * PAIR_ROWS);
-        a.desc[c] = make_int4(w.unit, w.head, piece_of(pl, line_end - 1), rows);
-      }
+      if (begins && !ends && rank == 0 && sw == 0 && lane == 0) describe(a, pl, w, c, PAIR_ROWS);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(l_o);
@@ -1031,68 +1105,66 @@ constexpr int JOIN_THREADS = 32 * JOIN_WARPS;
 constexpr int JOIN_WARP_PARTS = 6;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const BatchDev bt, const AttnDev a, const AttnShape sh) {
+__global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const AttnDev a, int rows) {
   constexpr int E = D / 32;  // dims per lane, in vectors of V
   constexpr int V = E >= 4 ? 4 : E;
   __shared__ float acc_sm[JOIN_WARPS][D];
-  __shared__ float sum_sm[JOIN_WARPS];
+  __shared__ float2 ml_sm[JOIN_WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are still written
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 ds = a.desc[c];
+  const int4 ds = a.desc[2 * c];
   if (ds.x < 0) return;
-  const int parts = ds.z - c + 1;
+  const int head0 = a.desc[2 * c + 1].x * a.group;
+  const int parts = ds.x - c + 1;
   const bool shared_row = parts > JOIN_WARP_PARTS;
-  const int step = shared_row ? JOIN_WARPS : 1, first = shared_row ? warp : 0;
-  AttnWalk w;
-  w.head = ds.y;
-  w.unit = ds.x;
-  w.t0 = 0;
-  w.left = 1;
-  walk_load(w, bt, a, sh);
-  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)); };
-  for (int r = blockIdx.y + (shared_row ? 0 : warp * gridDim.y); r < ds.w; r += gridDim.y * (shared_row ? 1 : JOIN_WARPS)) {
-    // the parts' maxima and sums, one lane each
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[slot_of(i) * sh.rows + r].x);
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[E];
+  const int step = shared_row ? JOIN_WARPS : 1;
+  for (int r = blockIdx.y + (shared_row ? 0 : warp * gridDim.y); r < ds.y; r += gridDim.y * (shared_row ? 1 : JOIN_WARPS)) {
+    float m = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    // joins one more (m, l, O); the loads of several parts are in flight at once
+    auto add = [&](float2 ml, const float *x) {
+      const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+      const float f0 = exp2_fast(m - ref), f1 = exp2_fast(ml.x - ref);
+      m = top;
+      sum = sum * f0 + f1 * ml.y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + f1 * x[e];
+    };
 #pragma unroll 4
-    for (int i = first; i < parts; i += step) {
-      const int64_t at = slot_of(i) * sh.rows + r;
+    for (int i = shared_row ? warp : 0; i < parts; i += step) {
+      const int64_t at = (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r;
       const float2 ml = a.part_ml[at];
-      const float f = exp2_fast(ml.x - ref);
-      sum = fmaf(f, ml.y, sum);
+      float x[E];
 #pragma unroll
-      for (int v = 0; v < E / V; ++v) {
-        const Vec<float, V> x = *reinterpret_cast<const Vec<float, V> *>(a.part_o + at * D + (v * 32 + lane) * V);
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[v * V + e] = fmaf(f, x.e[e], acc[v * V + e]);
-      }
+      for (int v = 0; v < E / V; ++v)
+        *reinterpret_cast<Vec<float, V> *>(x + v * V) =
+            *reinterpret_cast<const Vec<float, V> *>(a.part_o + at * D + (v * 32 + lane) * V);
+      add(ml, x);
     }
     if (shared_row) {
 #pragma unroll
       for (int v = 0; v < E / V; ++v)
 #pragma unroll
         for (int e = 0; e < V; ++e) acc_sm[warp][(v * 32 + lane) * V + e] = acc[v * V + e];
-      if (lane == 0) sum_sm[warp] = sum;
+      if (lane == 0) ml_sm[warp] = make_float2(m, sum);
       __syncthreads();
       if (warp == 0) {
 #pragma unroll
         for (int x = 1; x < JOIN_WARPS; ++x) {
-          sum += sum_sm[x];
+          float y[E];
 #pragma unroll
           for (int v = 0; v < E / V; ++v)
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[v * V + e] += acc_sm[x][(v * 32 + lane) * V + e];
+            for (int e = 0; e < V; ++e) y[v * V + e] = acc_sm[x][(v * 32 + lane) * V + e];
+          add(ml_sm[x], y);
         }
       }
     }
-    int64_t tok;
-    int head, sn;
-    if ((!shared_row || warp == 0) && unit_row(w, a, sh.rows, r, tok, head, sn)) {
+    if (!shared_row || warp == 0) {
+      const int i = ds.w + r, t = a.group_div.div(i);  // packed row of the sequence
+      const int64_t tok = (int64_t)ds.z + t;
+      const int head = head0 + i - t * a.group;
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       T *out = reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh;
 #pragma unroll
@@ -1103,7 +1175,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const BatchDev bt,
         *reinterpret_cast<Vec<T, V> *>(out + (v * 32 + lane) * V) = y;
       }
       if (a.lse && lane == 0)
-        a.lse[tok * a.heads + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        a.lse[tok * a.heads + head] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
     if (shared_row) __syncthreads();
   }
@@ -1141,7 +1213,7 @@ static AttnLayout attn_layout(int rows, int dim) {
   l.part_o = 0;
   l.part_ml = l.part_o + sizeof(float) * 2ull * workers * rows * dim;
   l.desc = l.part_ml + sizeof(float2) * 2ull * workers * rows;
-  l.total = l.desc + sizeof(int4) * workers;
+  l.total = l.desc + 2 * sizeof(int4) * workers;
   return l;
 }
 
@@ -1181,22 +1253,35 @@ static int allow_smem(const void *kern, int smem, int device, std::atomic<uint64
   return DCKV_OK;
 }
 
-// The join is launched with programmatic stream serialisation: its blocks are set up while the
-// first kernel ends and wait for its memory (griddepcontrol.wait).
-template <typename T, int D>
-static int run_join(const BatchDev &b, const AttnDev &a, const AttnShape &sh, int row_blocks, cudaStream_t st) {
+// Launches with programmatic stream serialisation: a kernel's blocks are set up while the kernel
+// before it in the stream ends, and wait for it (griddepcontrol.wait) before they read or write
+// global memory.
+static int launch_chained(const void *kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, void **args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.workers, (unsigned)row_blocks);
-  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  CK(cudaLaunchKernelEx(&cfg, k_attend_join<T, D>, b, a, sh));
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  CK(cudaLaunchKernelExC(&cfg, kern, args));
   ++g_launches;
   return DCKV_OK;
+}
+
+template <typename T, int D>
+static int run_join(const AttnDev &a, const AttnShape &sh, int row_blocks, cudaStream_t st) {
+  int rows = sh.rows;
+  void *args[] = {(void *)&a, (void *)&rows};
+  return launch_chained((const void *)k_attend_join<T, D>, dim3((unsigned)a.workers, (unsigned)row_blocks), JOIN_THREADS,
+                        0, 1, st, args);
 }
 
 template <typename T, int D, int NT>
@@ -1205,10 +1290,9 @@ static int run_attend_few(const CUtensorMap &mk, const CUtensorMap &mv, const Po
   auto kern = k_attend_few<T, D, NT>;
   static std::atomic<uint64_t> allowed{0};
   RET(allow_smem((const void *)kern, DecodeAttn<D, NT>::SMEM, device, allowed));
-  kern<<<a.workers, DEC_ATTN_THREADS, DecodeAttn<D, NT>::SMEM, st>>>(mk, mv, p, b, a, sh);
-  ++g_launches;
-  CK(cudaGetLastError());
-  return run_join<T, D>(b, a, sh, 8, st);
+  void *args[] = {(void *)&mk, (void *)&mv, (void *)&p, (void *)&b, (void *)&a, (void *)&sh};
+  RET(launch_chained((const void *)kern, dim3((unsigned)a.workers), DEC_ATTN_THREADS, DecodeAttn<D, NT>::SMEM, 1, st, args));
+  return run_join<T, D>(a, sh, 8, st);
 }
 
 template <typename T, int D>
@@ -1218,8 +1302,8 @@ static int run_attend_many(const CUtensorMap &mk, const CUtensorMap &mv, const P
   static std::atomic<uint64_t> allowed{0};
   RET(allow_smem((const void *)kern, PairAttn<D>::SMEM, device, allowed));
   void *args[] = {(void *)&mk, (void *)&mv, (void *)&p, (void *)&b, (void *)&a, (void *)&sh, (void *)&mp};
-  RET(launch_pairs((const void *)kern, a.workers, 2 * a.workers, PAIR_THREADS, PairAttn<D>::SMEM, st, args));
-  return run_join<T, D>(b, a, sh, 32, st);
+  RET(launch_chained((const void *)kern, dim3((unsigned)(2 * a.workers)), PAIR_THREADS, PairAttn<D>::SMEM, 2, st, args));
+  return run_join<T, D>(a, sh, 32, st);
 }
 
 template <typename T, int D>
