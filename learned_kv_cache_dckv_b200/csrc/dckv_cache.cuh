@@ -3,20 +3,25 @@
 // as codec rows.  Included by dckv.cu (error text, device scope, launch count).
 //
 // All three move each element once and do 3 flops on it at most, so HBM bounds them on long
-// inputs and the launch and a chain of dependent loads bound them on short ones.  One block
-// takes one token: its threads compute the token's (cos, sin) pairs once, into shared memory,
-// and every head (and layer) of the token reads them from there -- the fp64 reduction and
-// sincosf cost about as much as the whole copy if each head repeats them.  Elements move as
-// 16-byte vectors: a "chunk" is two vectors, the two halves of V pairs (half layout) or V whole
-// pairs (interleaved layout).
+// inputs and the launch and a chain of dependent loads bound them on short ones.  A block takes one
+// token: it looks its slot up and computes its (cos, sin) pairs once, into shared memory, and every
+// head (and layer) reads them from there -- the fp64 reduction and sincosf cost about as much as
+// the whole copy if each head repeats them.  Elements move as 16-byte vectors: a "chunk" is two
+// vectors, the two halves of V pairs (half layout) or V whole pairs (interleaved layout).
+// Blocks are small (128 threads) where there are many, so that some blocks' loads cover others'
+// look-ups.  Measured on four 4,096-token prompts, six layers, 207 MB (appended without a rotation)
+// and 258 MB (rows): 128 threads 41 and 53 us; 256 threads 45 and 59; a thread per chunk (384) 62
+// and 83; first chunk loaded before the look-up 48 and 58; four chunks ahead per thread 63 and 88;
+// four tokens per block 44-52 and 56-63; blocks of one layer's keys or values 53-65 and 111-119.
 #pragma once
 #include "../../include/dckv_cache.h"
 #include "dckv_epilogues.cuh"
 
 namespace dckv {
 
-constexpr int CACHE_THREADS = 128;  // DCKV_ROPE_MAX_PAIRS: one pair per thread
-static_assert(CACHE_THREADS >= DCKV_ROPE_MAX_PAIRS, "one (cos, sin) pair per thread");
+constexpr int CACHE_THREADS = 256;       // of a block, at most
+constexpr int CACHE_MANY_THREADS = 128;  // where the tokens fill the GPU
+constexpr int CACHE_MANY_TOKENS = 2368;  // sixteen blocks per SM
 
 // A rotation as the kernels take it (by value): mc and ms scale cos and sin (the magnitude, and
 // for the transpose the sign of sin).
@@ -82,6 +87,17 @@ struct alignas(V * sizeof(T)) Vec {
   T e[V];
 };
 
+// A vector that is read once: 16 bytes are fetched evict-first (rows of four prompts 53 -> 51 us).
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load_once(const T *p) {
+  if constexpr (sizeof(Vec<T, V>) == 16) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    return *reinterpret_cast<const Vec<T, V> *>(&v);
+  } else {
+    return *reinterpret_cast<const Vec<T, V> *>(p);
+  }
+}
+
 // Where chunk c of a rotated vector lies: its two V-element halves at off0 and off1 (off1 < 0:
 // absent, the odd last element of a scalar copy).  The first r / (2 V) chunks are pairs, the
 // rest copies.
@@ -135,51 +151,55 @@ __device__ __forceinline__ float2 rope_pair(const RopeDev &rope, int pos, int i)
   return make_float2(c * rope.mc, s * rope.ms);
 }
 
+// The (cos, sin) pairs of the block's token; all threads call it.
+__device__ __forceinline__ void fill_pairs(const RopeDev &rope, float2 *cs, int pos) {
+  for (int i = threadIdx.x; i < rope.r / 2; i += blockDim.x) cs[i] = rope_pair(rope, pos, i);
+  __syncthreads();
+}
+
 // ------------------------------------------------------------------ rotation of a tensor
 struct RopeArgs {
   const char *x;
   char *out;
   int64_t xt, xh, ot, oh;  // element strides: token, head
-  int64_t n;
-  int heads, dim;
-  int in_place;            // dims past rotary_dim already stand in out
+  int dim, chunks;         // chunks of a head that are moved (in place, dims past rotary_dim stand)
+  FastDiv chunk_div;
+  int per_token;           // heads * chunks
   const int32_t *positions;
 };
 
 template <typename T, int V>
 __global__ void __launch_bounds__(CACHE_THREADS) k_rope(const __grid_constant__ RopeDev rope, const RopeArgs a) {
   __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
-  const int chunks = a.in_place ? rope.r / (2 * V) : rope.r / (2 * V) + (a.dim - rope.r + 2 * V - 1) / (2 * V);
-  for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x) {
-    if (threadIdx.x < rope.r / 2) cs[threadIdx.x] = rope_pair(rope, __ldg(a.positions + t), threadIdx.x);
-    __syncthreads();
-    const T *x = reinterpret_cast<const T *>(a.x) + t * a.xt;
-    T *out = reinterpret_cast<T *>(a.out) + t * a.ot;
-    for (int it = threadIdx.x; it < a.heads * chunks; it += CACHE_THREADS) {
-      const int h = it / chunks, c = it - h * chunks;
-      int o0, o1;
-      const bool turn = chunk_at<V>(c, a.dim, rope, o0, o1);
-      Vec<T, V> x0 = *reinterpret_cast<const Vec<T, V> *>(x + h * a.xh + o0), x1 = x0;
-      if (o1 >= 0) x1 = *reinterpret_cast<const Vec<T, V> *>(x + h * a.xh + o1);
-      if (turn) rotate_chunk<T, V>(x0, x1, cs, c, rope.interleaved);
-      *reinterpret_cast<Vec<T, V> *>(out + h * a.oh + o0) = x0;
-      if (o1 >= 0) *reinterpret_cast<Vec<T, V> *>(out + h * a.oh + o1) = x1;
-    }
-    __syncthreads();
+  const int64_t t = blockIdx.x;
+  fill_pairs(rope, cs, __ldg(a.positions + t));
+  const T *x = reinterpret_cast<const T *>(a.x) + t * a.xt;
+  T *out = reinterpret_cast<T *>(a.out) + t * a.ot;
+  for (int i = threadIdx.x; i < a.per_token; i += blockDim.x) {
+    const int h = a.chunk_div.div(i), c = i - h * a.chunks;
+    int o0, o1;
+    const bool turn = chunk_at<V>(c, a.dim, rope, o0, o1);
+    Vec<T, V> x0 = load_once<T, V>(x + h * a.xh + o0), x1 = x0;
+    if (o1 >= 0) x1 = load_once<T, V>(x + h * a.xh + o1);
+    if (turn) rotate_chunk<T, V>(x0, x1, cs, c, rope.interleaved);
+    *reinterpret_cast<Vec<T, V> *>(out + h * a.oh + o0) = x0;
+    if (o1 >= 0) *reinterpret_cast<Vec<T, V> *>(out + h * a.oh + o1) = x1;
   }
 }
 
 // ------------------------------------------------------------------ tokens, sequences, slots
-// Sequence of token t (all threads of the block call it; -1: none).  A batch of up to four
-// offsets per thread is scanned with one load latency, a larger one bisected.
-__device__ __forceinline__ int find_sequence(const BatchDev &bt, int64_t t, int *shared_b) {
-  if (bt.batch <= 4 * CACHE_THREADS) {
-    if (threadIdx.x == 0) *shared_b = -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < bt.batch; b += CACHE_THREADS)
-      if (t >= __ldg(bt.offsets + b) && t < __ldg(bt.offsets + b + 1)) *shared_b = b;
-    __syncthreads();
-    return *shared_b;
+// Sequence of token t (-1: none), found by each warp for itself: a batch of up to four offsets per
+// lane is scanned with one load latency, a larger one bisected.
+__device__ __forceinline__ int find_sequence(const BatchDev &bt, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  if (bt.batch <= 128) {
+    int found = -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int b = lane + 32 * k;
+      if (b < bt.batch && t >= __ldg(bt.offsets + b) && t < __ldg(bt.offsets + b + 1)) found = b;
+    }
+    return __reduce_max_sync(0xffffffffu, found);
   }
   int lo = 0, hi = bt.batch;  // last b with offsets[b] <= t
   while (hi - lo > 1) {
@@ -200,51 +220,62 @@ __device__ __forceinline__ int64_t slot_page(const PoolDev &p, const BatchDev &b
   return page >= 0 && page < p.n_pages ? page : -1;
 }
 
+// Where a token's slot lies: page -1 where the token belongs to no sequence or is left out.
+struct TokenSlot {
+  int64_t page;
+  int row, pos;
+};
+
+// Looks up token t; last: its slot counted from the sequence's end (append), else from its start.
+__device__ __forceinline__ TokenSlot find_slot(const PoolDev &p, const BatchDev &bt, int64_t t, bool last,
+                                               const int32_t *positions, int32_t *status) {
+  TokenSlot s{-1, 0, 0};
+  const int b = find_sequence(bt, t);
+  if (b < 0) return s;
+  const int64_t first = __ldg(bt.offsets + b), n = __ldg(bt.offsets + b + 1) - first, len = __ldg(bt.kv_lens + b);
+  const int64_t j = last ? len - n + (t - first) : t - first;
+  s.page = slot_page(p, bt, b, j, s.row);
+  const bool ok = first >= 0 && first + n <= bt.n && (last ? n <= bt.max_new : j < len);
+  if (!ok) s.page = -1;
+  if (s.page < 0 && (threadIdx.x & 31) == 0) atomicExch(status, DCKV_ERANGE);
+  s.pos = positions ? __ldg(positions + t) : (int)j;
+  return s;
+}
+
 struct AppendDev {
   const char *k, *v, *q;
   char *q_out;
   int64_t kl, kt, kh, vl, vt, vh, qt, qh, ot, oh;
-  int n_q_heads;
+  int per_token;     // (2 layers * heads + q heads) * chunks
+  FastDiv head_div;  // by the pool's heads
   const int32_t *positions;
   int32_t *status;
 };
 
-// One token: its keys of every layer and head (rotated), its values (copied) and its queries
-// (rotated).
+// One token: its keys of every layer and head (rotated), values (copied) and queries (rotated).
 template <typename T, int V>
 __global__ void __launch_bounds__(CACHE_THREADS)
     k_append(const __grid_constant__ RopeDev rope, const PoolDev p, const BatchDev bt, const AppendDev a) {
   __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
-  __shared__ int shared_b;
   const int64_t t = blockIdx.x;
-  const int b = find_sequence(bt, t, &shared_b);
-  if (b < 0) return;
-  const int64_t first = __ldg(bt.offsets + b), n = __ldg(bt.offsets + b + 1) - first;
-  const int64_t j = (int64_t)__ldg(bt.kv_lens + b) - n + (t - first);
-  int row;
-  const int64_t page = slot_page(p, bt, b, j, row);
-  if (page < 0 || n > bt.max_new || first < 0 || first + n > bt.n) {
-    if (threadIdx.x == 0) atomicExch(a.status, DCKV_ERANGE);
-    return;
-  }
-  if (threadIdx.x < rope.r / 2)
-    cs[threadIdx.x] = rope_pair(rope, a.positions ? __ldg(a.positions + t) : (int)j, threadIdx.x);
-  __syncthreads();
-  const int chunks = p.dim / (2 * V);  // head_dim is a multiple of 2 V for both V
+  const TokenSlot s = find_slot(p, bt, t, true, a.positions, a.status);
+  if (s.page < 0) return;
+  if (rope.r) fill_pairs(rope, cs, s.pos);
+  const int shift = 31 - __clz(p.dim / (2 * V));  // chunks per vector: a power of two
   const int kv = p.n_layers * p.heads;
-  for (int it = threadIdx.x; it < (2 * kv + a.n_q_heads) * chunks; it += CACHE_THREADS) {
-    const int vec = it / chunks, c = it - vec * chunks;
+  for (int i = threadIdx.x; i < a.per_token; i += blockDim.x) {
+    const int vec = i >> shift, c = i - (vec << shift);
     const T *src;
     T *dst;
-    bool turn = rope.r > 0;
+    bool turn = true;
     if (vec < 2 * kv) {
       const bool is_v = vec >= kv;
-      const int lh = is_v ? vec - kv : vec, l = lh / p.heads, h = lh - l * p.heads;
+      const int lh = is_v ? vec - kv : vec, l = a.head_div.div(lh), h = lh - l * p.heads;
       src = is_v ? reinterpret_cast<const T *>(a.v) + l * a.vl + t * a.vt + h * a.vh
                  : reinterpret_cast<const T *>(a.k) + l * a.kl + t * a.kt + h * a.kh;
-      dst = is_v ? reinterpret_cast<T *>(p.v) + l * p.vl + page * p.vp + row * p.vr + h * p.vh
-                 : reinterpret_cast<T *>(p.k) + l * p.kl + page * p.kp + row * p.kr + h * p.kh;
-      turn = turn && !is_v;
+      dst = is_v ? reinterpret_cast<T *>(p.v) + l * p.vl + s.page * p.vp + s.row * p.vr + h * p.vh
+                 : reinterpret_cast<T *>(p.k) + l * p.kl + s.page * p.kp + s.row * p.kr + h * p.kh;
+      turn = !is_v;
     } else {
       const int h = vec - 2 * kv;
       src = reinterpret_cast<const T *>(a.q) + t * a.qt + h * a.qh;
@@ -252,47 +283,46 @@ __global__ void __launch_bounds__(CACHE_THREADS)
     }
     int o0, o1;
     const bool pairs = chunk_at<V>(c, p.dim, rope, o0, o1);
-    Vec<T, V> x0 = *reinterpret_cast<const Vec<T, V> *>(src + o0), x1 = *reinterpret_cast<const Vec<T, V> *>(src + o1);
+    Vec<T, V> x0 = load_once<T, V>(src + o0), x1 = load_once<T, V>(src + o1);
     if (turn && pairs) rotate_chunk<T, V>(x0, x1, cs, c, rope.interleaved);
     *reinterpret_cast<Vec<T, V> *>(dst + o0) = x0;
     *reinterpret_cast<Vec<T, V> *>(dst + o1) = x1;
   }
 }
 
+struct RowsDev {
+  char *rows;
+  int64_t row_stride;
+  int per_token;     // 2 layers * heads * chunks
+  FastDiv head_div;
+  const int32_t *positions;
+  int32_t *status;
+};
+
 // One slot of a prompt as a row [layer][K, V][head][dim], keys rotated back.
 template <typename T, int V>
 __global__ void __launch_bounds__(CACHE_THREADS)
-    k_rows(const __grid_constant__ RopeDev rope, const PoolDev p, const BatchDev bt, char *rows, int64_t row_stride,
-           const int32_t *positions, int32_t *status) {
+    k_rows(const __grid_constant__ RopeDev rope, const PoolDev p, const BatchDev bt, const RowsDev a) {
   __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
-  __shared__ int shared_b;
   const int64_t t = blockIdx.x;
-  const int b = find_sequence(bt, t, &shared_b);
-  if (b < 0) return;
-  const int64_t first = __ldg(bt.offsets + b), j = t - first;
-  int row;
-  const int64_t page = slot_page(p, bt, b, j, row);
-  if (page < 0 || j >= __ldg(bt.kv_lens + b) || first < 0 || __ldg(bt.offsets + b + 1) > bt.n) {
-    if (threadIdx.x == 0) atomicExch(status, DCKV_ERANGE);
-    return;
-  }
-  if (threadIdx.x < rope.r / 2)
-    cs[threadIdx.x] = rope_pair(rope, positions ? __ldg(positions + t) : (int)j, threadIdx.x);
-  __syncthreads();
-  const int chunks = p.dim / (2 * V);
-  T *out = reinterpret_cast<T *>(rows) + t * row_stride;
-  for (int it = threadIdx.x; it < 2 * p.n_layers * p.heads * chunks; it += CACHE_THREADS) {
-    const int vec = it / chunks, c = it - vec * chunks;  // vec = (layer * 2 + v) * heads + head
-    const int lv = vec / p.heads, h = vec - lv * p.heads, l = lv >> 1;
+  const TokenSlot s = find_slot(p, bt, t, false, a.positions, a.status);
+  if (s.page < 0) return;
+  if (rope.r) fill_pairs(rope, cs, s.pos);
+  const int shift = 31 - __clz(p.dim / (2 * V));
+  T *row = reinterpret_cast<T *>(a.rows) + t * a.row_stride;
+  for (int i = threadIdx.x; i < a.per_token; i += blockDim.x) {
+    const int vec = i >> shift, c = i - (vec << shift);  // vec = (layer * 2 + v) * heads + head
+    const int lv = a.head_div.div(vec), h = vec - lv * p.heads, l = lv >> 1;
     const bool is_v = lv & 1;
-    const T *src = is_v ? reinterpret_cast<const T *>(p.v) + l * p.vl + page * p.vp + row * p.vr + h * p.vh
-                        : reinterpret_cast<const T *>(p.k) + l * p.kl + page * p.kp + row * p.kr + h * p.kh;
+    const T *src = is_v ? reinterpret_cast<const T *>(p.v) + l * p.vl + s.page * p.vp + s.row * p.vr + h * p.vh
+                        : reinterpret_cast<const T *>(p.k) + l * p.kl + s.page * p.kp + s.row * p.kr + h * p.kh;
+    T *out = row + (int64_t)vec * p.dim;
     int o0, o1;
     const bool pairs = chunk_at<V>(c, p.dim, rope, o0, o1);
-    Vec<T, V> x0 = *reinterpret_cast<const Vec<T, V> *>(src + o0), x1 = *reinterpret_cast<const Vec<T, V> *>(src + o1);
+    Vec<T, V> x0 = load_once<T, V>(src + o0), x1 = load_once<T, V>(src + o1);
     if (!is_v && pairs) rotate_chunk<T, V>(x0, x1, cs, c, rope.interleaved);
-    *reinterpret_cast<Vec<T, V> *>(out + (int64_t)vec * p.dim + o0) = x0;
-    *reinterpret_cast<Vec<T, V> *>(out + (int64_t)vec * p.dim + o1) = x1;
+    *reinterpret_cast<Vec<T, V> *>(out + o0) = x0;
+    *reinterpret_cast<Vec<T, V> *>(out + o1) = x1;
   }
 }
 
@@ -378,6 +408,12 @@ static bool overlaps(const void *a, unsigned __int128 an, const void *b, unsigne
   return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
 }
 
+// Threads of a token's block: one per chunk up to a bound.
+static int block_threads(int64_t n, int per_token) {
+  const int most = n >= CACHE_MANY_TOKENS ? CACHE_MANY_THREADS : CACHE_THREADS;
+  return std::min(most, (per_token + 31) / 32 * 32);
+}
+
 // Whole vectors of v elements: pair chunks, copy chunks and every address.
 static bool rope_vectors(int r, int dim, int v) { return r % (2 * v) == 0 && (dim - r) % (2 * v) == 0; }
 
@@ -448,20 +484,25 @@ extern "C" int dckv_rope(const dckv_rope_spec *spec, int mode, const dckv_rope_a
   const int v = 16 / size;
   const bool vec = rope_vectors(rope.r, head_dim, v) && !(((uintptr_t)x | (uintptr_t)out) & 15) &&
                    !((x_token_stride | x_head_stride | out_token_stride | out_head_stride) % v);
+  const int vl = vec ? v : 1;
+  const int chunks = rope.r / (2 * vl) + (same ? 0 : (head_dim - rope.r + 2 * vl - 1) / (2 * vl));
+  const int64_t per_token = (int64_t)n_heads * chunks;
+  if (per_token > 0x7fffffffll - 2 * CACHE_THREADS) return fail(DCKV_EINVAL, "n_heads times head_dim is too large");
   const RopeArgs a{(const char *)x, (char *)out, x_token_stride, x_head_stride, out_token_stride, out_head_stride,
-                   n_tokens, n_heads, head_dim, same ? 1 : 0, positions};
+                   head_dim, chunks, FastDiv((uint32_t)chunks), (int)per_token, positions};
   cudaStream_t st = (cudaStream_t)stream;
   DEVICE_SCOPE(device);
   const unsigned grid = (unsigned)n_tokens;
+  const int threads = block_threads(n_tokens, (int)per_token);
   if (dtype == DCKV_FP32) {
-    if (vec) k_rope<float, 4><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
-    else k_rope<float, 1><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+    if (vec) k_rope<float, 4><<<grid, threads, 0, st>>>(rope, a);
+    else k_rope<float, 1><<<grid, threads, 0, st>>>(rope, a);
   } else if (dtype == DCKV_FP16) {
-    if (vec) k_rope<__half, 8><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
-    else k_rope<__half, 1><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+    if (vec) k_rope<__half, 8><<<grid, threads, 0, st>>>(rope, a);
+    else k_rope<__half, 1><<<grid, threads, 0, st>>>(rope, a);
   } else {
-    if (vec) k_rope<__nv_bfloat16, 8><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
-    else k_rope<__nv_bfloat16, 1><<<grid, CACHE_THREADS, 0, st>>>(rope, a);
+    if (vec) k_rope<__nv_bfloat16, 8><<<grid, threads, 0, st>>>(rope, a);
+    else k_rope<__nv_bfloat16, 1><<<grid, threads, 0, st>>>(rope, a);
   }
   ++g_launches;
   CK(cudaGetLastError());
@@ -488,10 +529,16 @@ extern "C" int dckv_cache_append(const dckv_kv_pool *pool, const dckv_cache_batc
       bad_stride(args->k_head_stride, p.heads, 8) || bad_stride(args->v_layer_stride, p.n_layers, 8) ||
       bad_stride(args->v_token_stride, n, 8) || bad_stride(args->v_head_stride, p.heads, 8))
     return fail(DCKV_EINVAL, "k and v strides must be positive multiples of 8 elements");
-  AppendDev a{(const char *)args->k, (const char *)args->v, nullptr, nullptr, args->k_layer_stride,
-              args->k_token_stride, args->k_head_stride, args->v_layer_stride, args->v_token_stride,
-              args->v_head_stride, args->q_token_stride, args->q_head_stride, args->q_out_token_stride,
-              args->q_out_head_stride, 0, args->positions, status};
+  AppendDev a = {};
+  a.k = (const char *)args->k;
+  a.v = (const char *)args->v;
+  a.kl = args->k_layer_stride, a.kt = args->k_token_stride, a.kh = args->k_head_stride;
+  a.vl = args->v_layer_stride, a.vt = args->v_token_stride, a.vh = args->v_head_stride;
+  a.qt = args->q_token_stride, a.qh = args->q_head_stride;
+  a.ot = args->q_out_token_stride, a.oh = args->q_out_head_stride;
+  a.positions = args->positions;
+  a.status = status;
+  int n_q_heads = 0;
   if (args->q) {
     const int hq = args->n_q_heads;
     if (!rope) return fail(DCKV_EINVAL, "q needs a rotation");
@@ -509,19 +556,22 @@ extern "C" int dckv_cache_append(const dckv_kv_pool *pool, const dckv_cache_batc
       return fail(DCKV_EINVAL, "q_out overlaps q without being q");
     a.q = (const char *)args->q;
     a.q_out = (char *)args->q_out;
-    a.n_q_heads = hq;
+    n_q_heads = hq;
   }
   if (n == 0) return DCKV_OK;
   cudaStream_t st = (cudaStream_t)stream;
   DEVICE_SCOPE(pool->device);
   const bool vec = rope_vectors(r.r, p.dim, 8);
-  // 16-bit types: the copies do not look at them, the rotation does
+  a.per_token = (2 * p.n_layers * p.heads + n_q_heads) * (p.dim / (vec ? 16 : 2));
+  a.head_div = FastDiv((uint32_t)p.heads);
+  const unsigned grid = (unsigned)n;
+  const int threads = block_threads(n, a.per_token);
   if (pool->dtype == DCKV_BF16) {
-    if (vec) k_append<__nv_bfloat16, 8><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
-    else k_append<__nv_bfloat16, 1><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
+    if (vec) k_append<__nv_bfloat16, 8><<<grid, threads, 0, st>>>(r, p, b, a);
+    else k_append<__nv_bfloat16, 1><<<grid, threads, 0, st>>>(r, p, b, a);
   } else {
-    if (vec) k_append<__half, 8><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
-    else k_append<__half, 1><<<(unsigned)n, CACHE_THREADS, 0, st>>>(r, p, b, a);
+    if (vec) k_append<__half, 8><<<grid, threads, 0, st>>>(r, p, b, a);
+    else k_append<__half, 1><<<grid, threads, 0, st>>>(r, p, b, a);
   }
   ++g_launches;
   CK(cudaGetLastError());
@@ -549,12 +599,21 @@ extern "C" int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch 
   cudaStream_t st = (cudaStream_t)stream;
   DEVICE_SCOPE(pool->device);
   const bool vec = rope_vectors(r.r, p.dim, 8);
+  RowsDev a = {};
+  a.rows = (char *)rows;
+  a.row_stride = row_stride;
+  a.per_token = 2 * p.n_layers * p.heads * (p.dim / (vec ? 16 : 2));
+  a.head_div = FastDiv((uint32_t)p.heads);
+  a.positions = positions;
+  a.status = status;
+  const unsigned grid = (unsigned)n_tokens;
+  const int threads = block_threads(n_tokens, a.per_token);
   if (pool->dtype == DCKV_BF16) {
-    if (vec) k_rows<__nv_bfloat16, 8><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
-    else k_rows<__nv_bfloat16, 1><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
+    if (vec) k_rows<__nv_bfloat16, 8><<<grid, threads, 0, st>>>(r, p, b, a);
+    else k_rows<__nv_bfloat16, 1><<<grid, threads, 0, st>>>(r, p, b, a);
   } else {
-    if (vec) k_rows<__half, 8><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
-    else k_rows<__half, 1><<<(unsigned)n_tokens, CACHE_THREADS, 0, st>>>(r, p, b, (char *)rows, row_stride, positions, status);
+    if (vec) k_rows<__half, 8><<<grid, threads, 0, st>>>(r, p, b, a);
+    else k_rows<__half, 1><<<grid, threads, 0, st>>>(r, p, b, a);
   }
   ++g_launches;
   CK(cudaGetLastError());
