@@ -150,12 +150,94 @@ __device__ __forceinline__ int last_worker(const AttnPlan &pl, const AttnWalk &w
   return (int)div_wide(end * pl.workers + pl.line - 1, pl.line) - 1;
 }
 
+// Worker c's part number k of its unit's n (parts), or its piece from tile `off` of its unit on.
+__device__ __forceinline__ void walk_part(AttnWalk &w, const AttnPlan &pl, const BatchDev &bt, const AttnDev &a,
+                                          const AttnShape &sh, int k) {
+  w.t0 = 0;
+  w.left = 0x7fffffff;
+  walk_load(w, bt, a, sh);
+  const int n = (w.tiles + pl.part - 1) / pl.part;
+  w.t0 = (int)((int64_t)w.tiles * k / n);
+  w.t1 = (int)((int64_t)w.tiles * (k + 1) / n);
+  w.left = w.t1 - w.t0;
+}
+
+// The plan of up to 32 units, made by each warp for itself, a unit per lane and in 32 bits: no
+// barrier, one load latency and little code (its instructions are fetched cold on every call).
+// Returns false where the numbers need the block's version below; any: c has a piece.
+__device__ __forceinline__ bool warp_plan(const BatchDev &bt, const AttnDev &a, const AttnShape &sh, int tries, int c,
+                                          AttnPlan &pl, AttnWalk &w, bool &any) {
+  const int lane = threadIdx.x & 31;
+  int t = 0;
+  if (lane < sh.units) {
+    const int b = sh.unit_div.div(lane);
+    SeqView s;
+    if (!load_seq(bt, sh.max_slots, b, s) && c == 0) atomicExch(a.status, DCKV_ERANGE);
+    t = unit_tiles(tile_seen(s, lane - b * sh.row_tiles, sh.rows, a), sh.key_tile);  // below 2^26
+  }
+  const uint32_t total = __reduce_add_sync(0xffffffffu, (uint32_t)t);
+  const uint64_t wide = (uint64_t)total * (uint32_t)sh.kv_heads;
+  if (wide >= (1u << 24)) return false;  // line * workers stays below 2^32
+  const uint32_t line = (uint32_t)wide, workers = max(1u, min((uint32_t)a.workers, line));
+  pl.line = line;
+  pl.workers = (int)workers;
+  pl.part = 0;
+  any = false;
+  if (line == 0) return true;
+  const uint32_t base = (line + workers - 1) / workers, step = max(1u, base >> 5);
+  int mine = t;
+  uint32_t pieces = 0;
+#pragma unroll 1
+  for (int j = 0; j < tries; ++j) {
+    const uint32_t part = base + j * step, n = (t + part - 1) / part;
+    pieces = __reduce_add_sync(0xffffffffu, n);
+    if (pieces * sh.kv_heads <= (uint32_t)a.workers) {
+      pl.part = (int)part;
+      pl.workers = (int)(pieces * sh.kv_heads);
+      mine = (int)n;
+      break;
+    }
+  }
+  if (c >= pl.workers) return true;
+  // the worker's start along the line of a head's parts or tiles
+  const uint32_t start = pl.part ? (uint32_t)c : (uint32_t)c * line / workers, period = pl.part ? pieces : total;
+  w.head = (int)(start / period);
+  const int pos = (int)(start - w.head * period);
+  int at = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  at -= mine;
+  const int from = __ffs(__ballot_sync(0xffffffffu, pos >= at && pos < at + mine)) - 1;
+  const int off = pos - __shfl_sync(0xffffffffu, at, from);
+  w.unit = from;
+  w.t0 = 0;
+  w.left = 0x7fffffff;
+  walk_load(w, bt, a, sh);
+  if (pl.part) {
+    const int n = (w.tiles + pl.part - 1) / pl.part;
+    w.t0 = (int)((uint32_t)w.tiles * off / n);
+    w.t1 = (int)((uint32_t)w.tiles * (off + 1) / n);
+    w.left = w.t1 - w.t0;
+  } else {
+    w.t0 = off;
+    w.left = (int)(((uint32_t)c + 1) * line / workers - start);
+    w.t1 = (int)min((int64_t)w.tiles, w.t0 + w.left);
+  }
+  any = true;
+  return true;
+}
+
 // Counts every unit's tiles (each thread a run of units, then a block scan), chooses the cut and
 // finds worker c's start.  Called by all threads of the block; returns false where c has no piece.
 // tries: cuts into parts to look at (1 .. PLAN_TRIES), part sizes from the stream's piece upwards.
 template <int THREADS>
 __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, const AttnShape &sh, int tries, int c,
                                           AttnPlanSmem *sm, AttnPlan &pl, AttnWalk &w) {
+  bool any;
+  if (sh.units <= 32 && warp_plan(bt, a, sh, tries, c, pl, w, any)) return any;
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (sh.units + THREADS - 1) / THREADS;
@@ -777,14 +859,16 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     tmem_alloc_pair(&tail->tmem_base, 512);
     tmem_relinquish_pair();
   }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // both CTAs' barriers are initialised before any cross-CTA signal
   asm volatile("griddepcontrol.wait;" ::: "memory");
   AttnPlan pl;
   AttnWalk w;
   const bool any = attn_plan<PAIR_THREADS>(bt, a, sh, PLAN_TRIES, c, plan_sm, pl, w);
-  if (threadIdx.x == 0 && rank == 0) a.desc[2 * c] = make_int4(-1, 0, 0, 0);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // both CTAs' barriers are initialised before any cross-CTA signal
+  if (threadIdx.x == 64 && rank == 0) a.desc[2 * c] = make_int4(-1, 0, 0, 0);  // by the thread that may describe
+  __syncthreads();  // the plan's shared memory is free
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = tail->tmem_base;
 

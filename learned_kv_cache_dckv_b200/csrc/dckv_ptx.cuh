@@ -310,6 +310,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// cluster_sync in two halves, with work in between.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Arrive on an mbarrier given by its shared::cluster address (own CTA or peer).  The
 // barriers signalled this way only hand TMEM back to the MMA issuer (ordered by the
 // tcgen05 fences), so the default CTA-scope semantics suffice.
