@@ -7,7 +7,8 @@
 // tiles, and the parts added at the end.
 //
 // Rows.  The g query heads of a KV head read the same keys, so a row tile packs (token, head of
-// the group) pairs: packed row i of a sequence is token i / g, head i % g.
+// the group) pairs: packed row i of a sequence is token i / g, head i % g.  The pairs' tiles hold
+// whole tokens (128 / g per CTA, the last rows idle where g does not divide 128).
 //
 // Work.  A unit is (KV head, sequence, row tile); its tiles are the key tiles that its last row
 // sees.  The units' tiles stand in one line, head after head, and every block takes an equal,
@@ -30,7 +31,7 @@ struct AttnDev {
   FastDiv group_div;
   float scale_log2;
   int32_t *status;
-  float *part_o;   // [2 workers][rows][dim]
+  float4 *part_o;  // [2 workers][rows][dim / 4] (few rows) or [2 workers][dim / 4][rows] (many)
   float2 *part_ml; // [2 workers][rows] (m, l)
   int4 *desc;      // [workers][2]: a split unit that begins here {last worker (-1: none), rows, first
                    // token, first packed row}, {KV head, ...}
@@ -738,7 +739,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
         if (a.lse && d == 0)
           a.lse[tok * a.heads + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
       } else {
-        *reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * C::ROWS + r) * D + d) = acc;
+        a.part_o[((int64_t)slot * C::ROWS + r) * (D / 4) + d / 4] = acc;
         if (d == 0) a.part_ml[slot * C::ROWS + r] = make_float2(top, sum);
       }
     }
@@ -798,20 +799,21 @@ struct PairBars {
   uint64_t pv_done;        // both: O += P V of a tile done.  S(j) complete implies O(j - 2) complete, so
                            // a warp at tile j may wait here for O(j - 1), not for any later one
   uint64_t o_full;         // both: the unit's last O += P V done
-  uint64_t q_full;         // leader: Q staged by every softmax warp
+  uint64_t q_empty;        // both: the unit's last S is computed, Q may be replaced
   uint64_t o_empty;        // leader: O read by every softmax warp
   uint64_t fix;            // own: a ragged V half landed
   GemmTail<STAGES> tail;
 };
 
 struct PairMaps {
-  int k_box, v_box;  // rows of one TMA box
+  int k_box, v_box;     // rows of one TMA box
+  int tokens, cta_rows; // of Q in one CTA's tile: tokens, tokens * group
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
-    k_attend_many(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PoolDev p,
-                  const BatchDev bt, const AttnDev a, const AttnShape sh, const PairMaps mp) {
+    k_attend_many(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_q, const PoolDev p, const BatchDev bt, const AttnDev a, const AttnShape sh, const PairMaps mp) {
   using C = PairAttn<D>;
   constexpr int STAGES = C::STAGES;
   constexpr uint32_t S_COL = 256;
@@ -846,7 +848,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->o_full, 1);
-    mbar_init(&bars->q_full, 2 * PAIR_SOFT_WARPS);
+    mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->o_empty, 2 * PAIR_SOFT_WARPS);
     mbar_init(&bars->fix, 1);
     mbar_init(&tail->drain_bar, 1);
@@ -854,6 +856,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     fence_mbar_init();
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_q);
   }
   if (warp == 1) {
     tmem_alloc_pair(&tail->tmem_base, 512);
@@ -878,10 +881,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     // ---------------------------------------------------------------- K and V (both CTAs)
     int stage = 0;
     uint32_t phase = 0;
-    uint32_t fixes = 0;
+    uint32_t fixes = 0, item = 0;
     bool ok = true;
-    // one item: tile t's K half or V half
-    auto load = [&](const AttnWalk &wk, int t, bool is_v) {
+    const uint32_t q_bytes = (uint32_t)mp.cta_rows * D * 2;
+    // one item: tile t's K half or V half; the unit's first K brings this CTA's rows of Q with it
+    auto load = [&](const AttnWalk &wk, int t, bool is_v, bool with_q) {
       const int key0 = t * PAIR_KEYS + (is_v ? 0 : (int)rank * 64);
       const int box = is_v ? mp.v_box : mp.k_box;
       const int groups = (is_v ? PAIR_KEYS : 64) / box, blocks = is_v ? C::V_BLOCKS : D / 64;
@@ -903,17 +907,26 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       // 0 * NaN is NaN, so they are cleared before the MMA sees them
       const int last_box = wk.s.len & ~(box - 1);  // first key of the box that holds slot `len`
       const bool ragged = is_v && last_box != wk.s.len && last_box >= key0 && last_box < key0 + PAIR_KEYS;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag));
+      ok = mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag);
+      if (ok && with_q && item > 0) ok = mbar_wait(&bars->q_empty, (item - 1) & 1u, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
+      const uint32_t bytes = C::BUF_BYTES + (with_q ? q_bytes : 0u);
       uint8_t *dst = bufs + stage * C::BUF_BYTES;
       const uint32_t fb = mapa_shared(smem_u32(&bars->full[stage]), 0);
       if (lane == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(&bars->full[stage], 2 * C::BUF_BYTES);
+        if (rank == 0) mbar_arrive_expect_tx(&bars->full[stage], 2 * bytes);
         if (ragged) mbar_arrive_expect_tx(&bars->fix, C::BUF_BYTES);
-        tail->ring[stage] = C::BUF_BYTES;
+        tail->ring[stage] = bytes;
         ++n_issued;
       }
       __syncwarp();
+      // rows past the sequence's are other tokens' or zeros; nothing of theirs is written
+      if (with_q && lane >= 32 - D / 64) {
+        const int x = lane - (32 - D / 64);
+        tma_load_3d_pair(q_sm + x * 16384, &tm_q, fb, 64 * x, wk.head * a.group,
+                         (int)wk.s.first + (2 * wk.rt + (int)rank) * mp.tokens);
+      }
       if (blk < blocks) {
         if (!is_v) {
           tma_load_4d_pair(dst + blk * 8192 + g * box * 128, &tm_k, fb, 64 * blk, row, wk.head, page);
@@ -943,13 +956,15 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       }
     };
     do {
-      load(w, w.t0, false);
+      load(w, w.t0, false, true);
       for (int t = w.t0; t < w.t1 && ok; ++t) {
-        if (t + 1 < w.t1) load(w, t + 1, false);
-        if (ok) load(w, t, true);
+        if (t + 1 < w.t1) load(w, t + 1, false, false);
+        if (ok) load(w, t, true, false);
       }
+      ++item;
     } while (ok && walk_next(w, bt, a, sh));
-    // every stage released: no commit is still in flight towards this CTA when it exits
+    // Q and every stage released: no commit is still in flight towards this CTA when it exits
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (item - 1) & 1u, abort_flag));
     for (int i = 0; i < STAGES && ok; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag));
       if (++stage == STAGES) {
@@ -984,13 +999,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
       };
       do {
-        ok = mbar_wait_cluster(&bars->q_full, item & 1u, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
         scores(tile);
         const int n = w.t1 - w.t0;
+        if (n == 1 && ok) umma_commit_pair(&bars->q_empty);
         for (int t = 0; t < n && ok; ++t, ++tile) {
           if (t + 1 < n) scores(tile + 1);
+          if (t + 2 == n && ok) umma_commit_pair(&bars->q_empty);
           if (ok && t == 0 && item > 0) ok = mbar_wait(&bars->o_empty, (item - 1) & 1u, abort_flag);
           if (ok) ok = mbar_wait(&bars->p_full[tile & 1u], (tile >> 1) & 1u, abort_flag);
           if (ok) ok = mbar_wait_cluster(&bars->full[stage], phase, abort_flag);
@@ -1019,34 +1033,15 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     const int row = quarter * 32 + lane;  // of this CTA's 128
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t l_p[2] = {mapa_shared(smem_u32(&bars->p_full[0]), 0), mapa_shared(smem_u32(&bars->p_full[1]), 0)};
-    const uint32_t l_q = mapa_shared(smem_u32(&bars->q_full), 0);
     const uint32_t l_o = mapa_shared(smem_u32(&bars->o_empty), 0);
     bool ok = true;
     uint32_t tile = 0, item = 0;
 
-    auto stage_q = [&](const AttnWalk &wk) {  // this CTA's 128 rows of Q, 16 rows per warp
-      constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks per row, rows per step
-      const int ch = lane % CH;
-#pragma unroll 8
-      for (int r0 = 0; r0 < 16; r0 += RPI) {
-        const int r = sw * 16 + r0 + lane / CH;
-        int64_t tok;
-        int head, sn;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (unit_row(wk, a, PAIR_ROWS, (int)rank * 128 + r, tok, head, sn))
-          v = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(a.q) + tok * a.qt + head * a.qh) + ch);
-        *reinterpret_cast<uint4 *>(q_sm + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_release(l_q);
-    };
-    stage_q(w);
-    bool more = true;
     do {
       int64_t tok = 0;
       int head = 0, seen = 0x7fffffff;
-      const bool valid = unit_row(w, a, PAIR_ROWS, (int)rank * 128 + row, tok, head, seen);
+      const int prow = (int)rank * mp.cta_rows + row;  // row of the pair's tile
+      const bool valid = row < mp.cta_rows && unit_row(w, a, sh.rows, prow, tok, head, seen);
       if (!valid) seen = 0x7fffffff;
       const bool work = __any_sync(0xffffffffu, valid);  // the same in both halves of the rows
       float ref = -INFINITY, sum = 0.f;  // ref in log2 units
@@ -1115,10 +1110,6 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(l_p[tile & 1u]);  // TMEM only: ordered by the tcgen05 fences
       }
-      // every S of this unit is computed, so Q may be replaced
-      AttnWalk nw = w;
-      more = walk_next(nw, bt, a, sh);
-      if (more) stage_q(nw);
       // the unit's end: join the halves' sums, read O
       float *xc = xch + (tile & 1u) * 256;
       xc[half * 128 + row] = sum;
@@ -1133,7 +1124,6 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       const int slot = begins ? 2 * c + 1 : 2 * c;
       const float inv = begins && ends ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
       if (work) {
-        const int64_t part = (int64_t)slot * PAIR_ROWS + rank * 128 + row;
 #pragma unroll 1
         for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
           uint32_t o[32];
@@ -1152,23 +1142,23 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
               *reinterpret_cast<uint4 *>(out + i) = v;
             }
           } else {
-            float *out = a.part_o + part * D + d;
+            float4 *out = a.part_o + ((int64_t)slot * (D / 4) + d / 4) * PAIR_ROWS + prow;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4 *>(out + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4 *>(out + (i / 4) * PAIR_ROWS) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
           __syncwarp();  // the next load is the whole warp's
         }
         if (valid && half == 0 && ok) {
-          if (!(begins && ends)) a.part_ml[part] = make_float2(ref, sum);
+          if (!(begins && ends)) a.part_ml[(int64_t)slot * PAIR_ROWS + prow] = make_float2(ref, sum);
           else if (a.lse) a.lse[tok * a.heads + head] = sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
         }
       }
-      if (begins && !ends && rank == 0 && sw == 0 && lane == 0) describe(a, pl, w, c, PAIR_ROWS);
+      if (begins && !ends && rank == 0 && sw == 0 && lane == 0) describe(a, pl, w, c, sh.rows);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(l_o);
-      w = nw;
-    } while (more);
+    } while (walk_next(w, bt, a, sh));
   }
   __syncthreads();
   pair_teardown<STAGES>(tail, bars->full, n_issued, rank, warp, lane, a.status);
@@ -1181,15 +1171,16 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 // ------------------------------------------------------------------ joining split units
 // Block (c, y): if a unit begins in worker c's piece and is split, joins its rows y, y + gridDim.y, ...
 // Parts: slot 2 c + 1 (the beginning), then slot 2 i of the workers i up to the last.  With few
-// parts (many rows) each of the eight warps joins a row by itself; with more than
-// JOIN_WARP_PARTS the warps share a row, every eighth part each, and add up in shared memory: one
-// warp alone would wait for the parts one load latency after the other.
+// parts each of the eight warps joins a row by itself; with more than JOIN_WARP_PARTS the warps
+// share a row, every eighth part each, and add up in shared memory: one warp alone would wait for
+// the parts one load latency after the other.
+// Few rows: parts are [rows][dim], a warp reads a row's dims side by side.
 constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_THREADS = 32 * JOIN_WARPS;
 constexpr int JOIN_WARP_PARTS = 6;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const AttnDev a, int rows) {
+__global__ void __launch_bounds__(JOIN_THREADS) k_join_few(const AttnDev a, int rows) {
   constexpr int E = D / 32;  // dims per lane, in vectors of V
   constexpr int V = E >= 4 ? 4 : E;
   __shared__ float acc_sm[JOIN_WARPS][D];
@@ -1223,7 +1214,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const AttnDev a, i
 #pragma unroll
       for (int v = 0; v < E / V; ++v)
         *reinterpret_cast<Vec<float, V> *>(x + v * V) =
-            *reinterpret_cast<const Vec<float, V> *>(a.part_o + at * D + (v * 32 + lane) * V);
+            *reinterpret_cast<const Vec<float, V> *>(reinterpret_cast<const float *>(a.part_o) + at * D + (v * 32 + lane) * V);
       add(ml, x);
     }
     if (shared_row) {
@@ -1265,6 +1256,106 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attend_join(const AttnDev a, i
   }
 }
 
+// Many rows: parts are [dim / 4][rows], as the softmax threads hold them (a row per lane; stores of
+// [rows][dim] took 2.3 us of a 64 KB part, 32 lines per store).  A warp joins eight rows at a time
+// and JOIN_STEPS values of k: lane = row + 8 q reads the dims 16 k + 4 q .. + 3 of its row, 128 bytes
+// of eight rows side by side per q.  (With this layout and join the few rows' cases took 2 us longer.)
+constexpr int JOIN_STEPS = 4;
+
+// (m, l, O) of one row's dims in this lane.
+struct JoinAcc {
+  static constexpr int K = JOIN_STEPS;
+  float m = -INFINITY, l = 0.f;
+  float4 o[K];
+  __device__ __forceinline__ JoinAcc() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(float2 ml, const float4 (&x)[K]) {
+    const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+    const float f0 = exp2_fast(m - ref), f1 = exp2_fast(ml.x - ref);
+    m = top;
+    l = l * f0 + f1 * ml.y;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      o[k].x = o[k].x * f0 + f1 * x[k].x;
+      o[k].y = o[k].y * f0 + f1 * x[k].y;
+      o[k].z = o[k].z * f0 + f1 * x[k].z;
+      o[k].w = o[k].w * f0 + f1 * x[k].w;
+    }
+  }
+};
+
+// Adds the parts first, first + step, ... of row r, dims 16 (k0 + k) + 4 q.
+template <int D>
+__device__ __forceinline__ void join_parts(JoinAcc &acc, const AttnDev &a, int rows, int c, int parts, int first,
+                                           int step, int r, int q, int k0) {
+  constexpr int K = JOIN_STEPS;
+#pragma unroll 4
+  for (int i = first; i < parts; i += step) {
+    const int64_t slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
+    float4 x[K];
+    const float2 ml = a.part_ml[slot * rows + r];
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = a.part_o[(slot * (D / 4) + (k0 + k) * 4 + q) * rows + r];
+    acc.add(ml, x);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void join_store(const JoinAcc &acc, const AttnDev &a, int4 ds, int head0, int r, int q,
+                                           int k0) {
+  const int i = ds.w + r, t = a.group_div.div(i);  // packed row of the sequence
+  const int64_t tok = (int64_t)ds.z + t;
+  const int head = head0 + i - t * a.group;
+  const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
+  T *out = reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh + k0 * 16 + q * 4;
+#pragma unroll
+  for (int k = 0; k < JOIN_STEPS; ++k)
+    store4<T>(out + k * 16, make_float4(acc.o[k].x * inv, acc.o[k].y * inv, acc.o[k].z * inv, acc.o[k].w * inv));
+  if (a.lse && q == 0 && k0 == 0)
+    a.lse[tok * a.heads + head] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_THREADS) k_join_many(const AttnDev a, int rows) {
+  constexpr int CHUNKS = D / 16 / JOIN_STEPS;
+  __shared__ float4 acc_sm[JOIN_WARPS][JOIN_STEPS][32];
+  __shared__ float2 ml_sm[JOIN_WARPS][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are still written
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 3;
+  const int4 ds = a.desc[2 * c];
+  if (ds.x < 0) return;
+  const int head0 = a.desc[2 * c + 1].x * a.group;
+  const int parts = ds.x - c + 1, tasks = ((ds.y + 7) >> 3) * CHUNKS;
+  const bool shared_task = parts > JOIN_WARP_PARTS;
+  const int first = shared_task ? warp : 0, step = shared_task ? JOIN_WARPS : 1;
+  for (int task = shared_task ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp; task < tasks;
+       task += gridDim.y * (shared_task ? 1 : JOIN_WARPS)) {
+    const int g = task / CHUNKS, k0 = (task - g * CHUNKS) * JOIN_STEPS, row = g * 8 + (lane & 7);
+    const int r = min(row, ds.y - 1);
+    JoinAcc acc;
+    join_parts<D>(acc, a, rows, c, parts, first, step, r, q, k0);
+    if (shared_task) {
+#pragma unroll
+      for (int k = 0; k < JOIN_STEPS; ++k) acc_sm[warp][k][lane] = acc.o[k];
+      ml_sm[warp][lane] = make_float2(acc.m, acc.l);
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int x = 1; x < JOIN_WARPS; ++x) {
+          float4 y[JOIN_STEPS];
+#pragma unroll
+          for (int k = 0; k < JOIN_STEPS; ++k) y[k] = acc_sm[x][k][lane];
+          acc.add(ml_sm[x][lane], y);
+        }
+      }
+    }
+    if ((!shared_task || warp == 0) && row < ds.y) join_store<T>(acc, a, ds, head0, r, q, k0);
+    if (shared_task) __syncthreads();
+  }
+}
+
 }  // namespace dckv
 
 // ============================================================================ host
@@ -1291,7 +1382,7 @@ struct AttnLayout {
   size_t part_o, part_ml, desc, total;
 };
 
-static AttnLayout attn_layout(int rows, int dim) {
+static AttnLayout attn_layout(int rows, int dim) {  // rows: 8, 16 or PAIR_ROWS
   const int workers = rows == PAIR_ROWS ? ATTN_MAX_PAIRS : ATTN_MAX_WORKERS;
   AttnLayout l;
   l.part_o = 0;
@@ -1302,10 +1393,27 @@ static AttnLayout attn_layout(int rows, int dim) {
 }
 
 // Rows of a tile: 8 or 16 where every sequence's packed rows fit (k_attend_few), else a pair's
-// 256 (k_attend_many).
+// 256 (k_attend_many).  A group of more than 128 heads does not fit a CTA's rows and takes tiles
+// of 16, several per token.
 static int attn_rows(const BatchDev &b, int group) {
   const int64_t rows = (int64_t)b.max_new * group;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : PAIR_ROWS;
+  return rows <= 8 ? 8 : rows <= 16 || group > 128 ? 16 : PAIR_ROWS;
+}
+
+// Q as [tokens][heads][dim]; box: 64 dims x a group's heads x the tokens of one CTA's tile.
+static int map_queries(CUtensorMap *m, const void *q, bool bf16, int dim, int heads, int64_t n, int64_t hs, int64_t ts,
+                       int group, int tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(DCKV_ECUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)n};
+  cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? hs : 8) * 2, (cuuint64_t)(n > 1 ? ts : 8) * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(q),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DCKV_ECUDA, "tensor map (queries) encode failed: %d", (int)r);
+  return DCKV_OK;
 }
 
 extern "C" size_t dckv_attention_workspace_bytes(const dckv_kv_pool *pool, const dckv_cache_batch *batch, int n_q_heads) {
@@ -1360,12 +1468,9 @@ static int launch_chained(const void *kern, dim3 grid, int threads, int smem, in
   return DCKV_OK;
 }
 
-template <typename T, int D>
-static int run_join(const AttnDev &a, const AttnShape &sh, int row_blocks, cudaStream_t st) {
-  int rows = sh.rows;
+static int run_join(const void *kern, const AttnDev &a, int rows, int row_blocks, cudaStream_t st) {
   void *args[] = {(void *)&a, (void *)&rows};
-  return launch_chained((const void *)k_attend_join<T, D>, dim3((unsigned)a.workers, (unsigned)row_blocks), JOIN_THREADS,
-                        0, 1, st, args);
+  return launch_chained(kern, dim3((unsigned)a.workers, (unsigned)row_blocks), JOIN_THREADS, 0, 1, st, args);
 }
 
 template <typename T, int D, int NT>
@@ -1376,26 +1481,26 @@ static int run_attend_few(const CUtensorMap &mk, const CUtensorMap &mv, const Po
   RET(allow_smem((const void *)kern, DecodeAttn<D, NT>::SMEM, device, allowed));
   void *args[] = {(void *)&mk, (void *)&mv, (void *)&p, (void *)&b, (void *)&a, (void *)&sh};
   RET(launch_chained((const void *)kern, dim3((unsigned)a.workers), DEC_ATTN_THREADS, DecodeAttn<D, NT>::SMEM, 1, st, args));
-  return run_join<T, D>(a, sh, 8, st);
+  return run_join((const void *)k_join_few<T, D>, a, 8 * NT, 8, st);
 }
 
 template <typename T, int D>
-static int run_attend_many(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
+static int run_attend_many(const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mq, const PoolDev &p, const BatchDev &b,
                            const AttnDev &a, const AttnShape &sh, const PairMaps &mp, int device, cudaStream_t st) {
   auto kern = k_attend_many<T, D>;
   static std::atomic<uint64_t> allowed{0};
   RET(allow_smem((const void *)kern, PairAttn<D>::SMEM, device, allowed));
-  void *args[] = {(void *)&mk, (void *)&mv, (void *)&p, (void *)&b, (void *)&a, (void *)&sh, (void *)&mp};
+  void *args[] = {(void *)&mk, (void *)&mv, (void *)&mq, (void *)&p, (void *)&b, (void *)&a, (void *)&sh, (void *)&mp};
   RET(launch_chained((const void *)kern, dim3((unsigned)(2 * a.workers)), PAIR_THREADS, PairAttn<D>::SMEM, 2, st, args));
-  return run_join<T, D>(a, sh, 32, st);
+  return run_join((const void *)k_join_many<T, D>, a, PAIR_ROWS, 16, st);
 }
 
 template <typename T, int D>
-static int run_attend(const CUtensorMap &mk, const CUtensorMap &mv, const PoolDev &p, const BatchDev &b,
+static int run_attend(const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mq, const PoolDev &p, const BatchDev &b,
                       const AttnDev &a, const AttnShape &sh, const PairMaps &mp, int device, cudaStream_t st) {
   if (sh.rows == 8) return run_attend_few<T, D, 1>(mk, mv, p, b, a, sh, device, st);
   if (sh.rows == 16) return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, device, st);
-  return run_attend_many<T, D>(mk, mv, p, b, a, sh, mp, device, st);
+  return run_attend_many<T, D>(mk, mv, mq, p, b, a, sh, mp, device, st);
 }
 
 // Rows of a TMA box: the largest power of two up to `most` that divides a page, so that no box
@@ -1433,8 +1538,10 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
     return fail(DCKV_EINVAL, "out overlaps q");
   const int group = hq / p.heads;
   AttnShape sh;
-  sh.rows = attn_rows(b, group);
-  const bool many = sh.rows == PAIR_ROWS;
+  const int slot_rows = attn_rows(b, group);  // of the workspace's parts
+  const bool many = slot_rows == PAIR_ROWS;
+  const int cta_tokens = many ? 128 / group : 0;
+  sh.rows = many ? 2 * cta_tokens * group : slot_rows;
   sh.key_tile = many ? PAIR_KEYS : DEC_KEY_TILE;
   sh.kv_heads = p.heads;
   const int64_t most_rows = std::min<int64_t>(b.max_new, std::max<int64_t>(n, 1)) * group;
@@ -1445,7 +1552,7 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   sh.unit_div = FastDiv((uint32_t)row_tiles);
   sh.units = (int)(row_tiles * b.batch);
   sh.max_slots = std::min<int64_t>((int64_t)b.max_pages * p.page_size, 0x7fffffffll - 65536);
-  const AttnLayout lay = attn_layout(sh.rows, p.dim);
+  const AttnLayout lay = attn_layout(slot_rows, p.dim);
   if (ws_bytes < lay.total) return fail(DCKV_ECAPACITY, "workspace too small (%zu < %zu)", ws_bytes, lay.total);
   if (n == 0) return DCKV_OK;
   cudaStream_t st = (cudaStream_t)stream;
@@ -1454,20 +1561,23 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   RET(sm_count(pool->device, sms));
   char *ws = (char *)workspace;
   const AttnDev a{(const char *)args->q, (char *)args->out, args->lse, qt, qh, ot, oh, hq, group, args->causal,
-                  FastDiv((uint32_t)group), args->scale * 1.4426950408889634f, status, (float *)(ws + lay.part_o), (float2 *)(ws + lay.part_ml),
+                  FastDiv((uint32_t)group), args->scale * 1.4426950408889634f, status, (float4 *)(ws + lay.part_o), (float2 *)(ws + lay.part_ml),
                   (int4 *)(ws + lay.desc),
                   many ? std::min(sms / 2, ATTN_MAX_PAIRS) : std::min(sms, ATTN_MAX_WORKERS)};
   const bool bf = pool->dtype == DCKV_BF16;
   CUtensorMap mk, mv;
-  const PairMaps mp{many ? box_rows(p.page_size, 64) : DEC_SLICE, many ? box_rows(p.page_size, PAIR_KEYS) : DEC_SLICE};
+  const PairMaps mp{many ? box_rows(p.page_size, 64) : DEC_SLICE, many ? box_rows(p.page_size, PAIR_KEYS) : DEC_SLICE,
+                    cta_tokens, cta_tokens * group};
+  CUtensorMap mq{};
+  if (many) RET(map_queries(&mq, args->q, bf, p.dim, hq, n, qh, qt, group, cta_tokens));
   RET(map_pages(&mk, p.k + 2 * args->layer * p.kl, bf, p, p.kr, p.kh, p.kp, mp.k_box));
   RET(map_pages(&mv, p.v + 2 * args->layer * p.vl, bf, p, p.vr, p.vh, p.vp, mp.v_box, many && p.dim == 64 ? 32 : 64));
   if (p.dim == 64)
-    return bf ? run_attend<__nv_bfloat16, 64>(mk, mv, p, b, a, sh, mp, pool->device, st)
-              : run_attend<__half, 64>(mk, mv, p, b, a, sh, mp, pool->device, st);
+    return bf ? run_attend<__nv_bfloat16, 64>(mk, mv, mq, p, b, a, sh, mp, pool->device, st)
+              : run_attend<__half, 64>(mk, mv, mq, p, b, a, sh, mp, pool->device, st);
   if (p.dim == 128)
-    return bf ? run_attend<__nv_bfloat16, 128>(mk, mv, p, b, a, sh, mp, pool->device, st)
-              : run_attend<__half, 128>(mk, mv, p, b, a, sh, mp, pool->device, st);
-  return bf ? run_attend<__nv_bfloat16, 256>(mk, mv, p, b, a, sh, mp, pool->device, st)
-            : run_attend<__half, 256>(mk, mv, p, b, a, sh, mp, pool->device, st);
+    return bf ? run_attend<__nv_bfloat16, 128>(mk, mv, mq, p, b, a, sh, mp, pool->device, st)
+              : run_attend<__half, 128>(mk, mv, mq, p, b, a, sh, mp, pool->device, st);
+  return bf ? run_attend<__nv_bfloat16, 256>(mk, mv, mq, p, b, a, sh, mp, pool->device, st)
+            : run_attend<__half, 256>(mk, mv, mq, p, b, a, sh, mp, pool->device, st);
 }

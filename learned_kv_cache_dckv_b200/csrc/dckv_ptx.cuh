@@ -83,8 +83,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
-// The same wait with cluster scope: what the peer CTA wrote before its release arrive (to its
-// own shared memory or TMEM) is ordered before the operations after this wait.
+// The same wait with cluster scope: what the peer CTA wrote to its own shared memory before it
+// completed the phase (mbar_complete_tx_cluster) is ordered before the operations after this wait.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -349,11 +349,6 @@ __device__ __forceinline__ void tma_load_4d_pair(void *dst, const void *tmap, ui
       "%5, %6}], [%2];" ::"r"(smem_u32(dst)),
       "l"(tmap), "r"(bar_cl), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
-}
-
-// Arrive with release at cluster scope (see mbar_wait_cluster), own CTA or peer.
-__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cl_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 
 // Completes `bytes` of the transaction count of an mbarrier in either CTA of the cluster, after
