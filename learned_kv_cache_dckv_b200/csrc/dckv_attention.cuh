@@ -366,6 +366,28 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp and flush to zer
   return y;
 }
 
+// Two fp32 values in one register pair, and sm_100's packed arithmetic on them.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 un2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
@@ -1093,16 +1115,20 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           }
           const float off = ref == -INFINITY ? 0.f : -ref;
           uint32_t pk[32];
-          float s2[2] = {0.f, 0.f};
+          uint64_t sum2 = f2(0.f, 0.f);
+          const uint64_t scale2 = f2(a.scale_log2, a.scale_log2), off2 = f2(off, off);
+          // Packed multiply-adds: 408 -> 396 us on 2,048 tokens over 32,768 slots.  Taking every second
+          // to fourth pair's exp2 off the special-function unit (a polynomial on the FMA pipe) made
+          // dim 128 slower, 415 -> 428-451 us: instruction issue bounds this phase, not that unit.
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float e0 = exp2_fast(fmaf(__uint_as_float(x[2 * i]), a.scale_log2, off));
-            const float e1 = exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), a.scale_log2, off));
-            s2[0] += e0;
-            s2[1] += e1;
+            const float2 y = un2(fma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, off2));
+            const float e0 = exp2_fast(y.x), e1 = exp2_fast(y.y);
+            sum2 = add2(sum2, f2(e0, e1));
             pk[i] = pack2<T>(e0, e1);
           }
-          sum += s2[0] + s2[1];
+          const float2 two = un2(sum2);
+          sum += two.x + two.y;
           tmem_st_32x32b_x32(sb + half * 32, pk);
           tmem_st_wait();
         }
