@@ -784,7 +784,8 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
 // stream a whole K and V tile per 128 rows, 128 bytes per clock at the tensor rate and dim 256;
 // the pair needs half of that per SM, what L2 gives.
 // TMEM (512 columns): O in the first `dim`, then two S tiles of 128 columns; P overwrites the
-// first half of its own S tile as 16-bit pairs and is the A operand of the second product.
+// first half of its own S tile as 16-bit pairs and is the A operand of the second product.  (One S
+// tile, freed once it is in registers, and two P tiles of their own measured the same.)
 // Roles, per CTA: warp 0 loads K and V halves (lanes issue one TMA box each, through the page
 // table), warp 1 of the even CTA issues all MMAs, warps 2-9 are the softmax: two threads per
 // row, 64 columns each, which exchange the row maximum through shared memory.  While they work
@@ -824,6 +825,7 @@ struct PairBars {
   uint64_t q_empty;        // both: the unit's last S is computed, Q may be replaced
   uint64_t o_empty;        // leader: O read by every softmax warp
   uint64_t fix;            // own: a ragged V half landed
+  uint64_t mma_end;        // after a timed-out wait: the MMAs issued so far are done
   GemmTail<STAGES> tail;
 };
 
@@ -854,7 +856,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   AttnPlanSmem *plan_sm = reinterpret_cast<AttnPlanSmem *>(xch);
   GemmTail<STAGES> *tail = &bars->tail;
   volatile int *abort_flag = &tail->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp-uniform values, and known to be
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int c = blockIdx.x >> 1;
   uint32_t n_issued = 0;
@@ -873,6 +876,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->o_empty, 2 * PAIR_SOFT_WARPS);
     mbar_init(&bars->fix, 1);
+    mbar_init(&bars->mma_end, 1);
     mbar_init(&tail->drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -895,7 +899,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   __syncthreads();  // the plan's shared memory is free
   cluster_wait();
   tc_fence_after();
-  const uint32_t tmem = tail->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tail->tmem_base, 0);
 
   if (!any) {
     // no piece: straight to the teardown (both CTAs of the pair alike)
@@ -996,25 +1000,34 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (even CTA)
-    if (lane == 0 && rank == 0) {
+    // The whole warp runs the loop in step and one elected lane issues under a predicate, so that the
+    // operands stay in uniform registers (one lane in a branch of its own took 70 clocks per MMA, 24 of
+    // them a tile at dim 256; three chunks of up to 300 tokens over 4,000 slots 33.3 -> 31.5 us).
+    // Descriptors are a base plus constants (addresses advance in the low word's first 14 bits, which
+    // never carry out of them).
+    if (rank == 0) {
       constexpr int BF = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
       const uint32_t id_s = idesc_f16(BF, PAIR_ROWS, PAIR_KEYS);
       const uint32_t id_o = idesc_f16(BF, PAIR_ROWS, D) | IDESC_B_MN_MAJOR;
-      const uint32_t q0 = smem_u32(q_sm);
+      const uint32_t issue = elect_one();
+      const uint64_t q_desc = sw128_desc(smem_u32(q_sm));
+      const uint64_t k_desc0 = sw128_desc(smem_u32(bufs));
+      const uint64_t v_desc0 = mn_desc(smem_u32(bufs), C::V_ROW, PAIR_KEYS * C::V_ROW);
       int stage = 0;
       uint32_t phase = 0, tile = 0, item = 0;
       bool ok = true;
       auto scores = [&](uint32_t j) {  // S tile j of the kernel
-        ok = mbar_wait(&bars->full[stage], phase, abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[stage], phase, abort_flag));
         if (!ok) return;
         tc_fence_after();
-        const uint32_t kb = smem_u32(bufs + stage * C::BUF_BYTES);
+        const uint64_t kd = k_desc0 + (uint64_t)(uint32_t)(stage * (C::BUF_BYTES >> 4));
+        const uint32_t d = tmem + S_COL + (j & 1u) * PAIR_KEYS;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16_pair(tmem + S_COL + (j & 1u) * PAIR_KEYS, sw128_desc(q0 + (kk >> 2) * 16384 + (kk & 3) * 32),
-                        sw128_desc(kb + (kk >> 2) * 8192 + (kk & 3) * 32), id_s, kk > 0);
-        umma_commit_pair(&bars->empty[stage]);
-        umma_commit_pair(&bars->s_full[j & 1u]);
+          umma_f16_pair_if(issue, d, q_desc + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                           kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_s, kk > 0);
+        umma_commit_pair_if(issue, &bars->empty[stage]);
+        umma_commit_pair_if(issue, &bars->s_full[j & 1u]);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -1023,24 +1036,25 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       do {
         scores(tile);
         const int n = w.t1 - w.t0;
-        if (n == 1 && ok) umma_commit_pair(&bars->q_empty);
+        if (n == 1 && ok) umma_commit_pair_if(issue, &bars->q_empty);
         for (int t = 0; t < n && ok; ++t, ++tile) {
           if (t + 1 < n) scores(tile + 1);
-          if (t + 2 == n && ok) umma_commit_pair(&bars->q_empty);
+          if (t + 2 == n && ok) umma_commit_pair_if(issue, &bars->q_empty);
           if (ok && t == 0 && item > 0) ok = mbar_wait(&bars->o_empty, (item - 1) & 1u, abort_flag);
           if (ok) ok = mbar_wait(&bars->p_full[tile & 1u], (tile >> 1) & 1u, abort_flag);
           if (ok) ok = mbar_wait_cluster(&bars->full[stage], phase, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t vb = smem_u32(bufs + stage * C::BUF_BYTES);
+          const uint64_t vd = v_desc0 + (uint64_t)(uint32_t)(stage * (C::BUF_BYTES >> 4));
           const uint32_t pt = tmem + S_COL + (tile & 1u) * PAIR_KEYS;
+          const uint32_t acc = t > 0;
 #pragma unroll
           for (int kk = 0; kk < PAIR_KEYS / 16; ++kk)
-            umma_f16_pair_ts(tmem, pt + kk * 8, mn_desc(vb + kk * 16 * C::V_ROW, C::V_ROW, PAIR_KEYS * C::V_ROW), id_o,
-                             t > 0 || kk > 0);
-          umma_commit_pair(&bars->empty[stage]);
-          umma_commit_pair(&bars->pv_done);
-          if (t + 1 == n) umma_commit_pair(&bars->o_full);
+            umma_f16_pair_ts_if(issue, tmem, pt + kk * 8, vd + ((kk * 16 * C::V_ROW) >> 4), id_o, kk > 0 ? 1u : acc);
+          umma_commit_pair_if(issue, &bars->empty[stage]);
+          umma_commit_pair_if(issue, &bars->pv_done);
+          if (t + 1 == n) umma_commit_pair_if(issue, &bars->o_full);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -1048,6 +1062,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
         ++item;
       } while (ok && walk_next(w, bt, a, sh));
+      if (!ok) {  // leave no MMA in flight (the commit counts the issuing lane's)
+        umma_commit_pair_if(issue, &bars->mma_end);
+        mbar_drain(&bars->mma_end, 0);
+      }
     }
   } else {
     // ---------------------------------------------------------------- softmax (both CTAs)
