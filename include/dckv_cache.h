@@ -22,8 +22,9 @@
  * Status.  *status (device int32) is written only when an error is found on the device
  * (unlike dckv_encode's, which every call overwrites): set it to 0 once, and one word can
  * collect the errors of many calls.  DCKV_ERANGE: a length, offset or page index is outside
- * its bounds (the tokens concerned are left out, nothing is read or written out of bounds);
- * DCKV_ETIMEOUT as in dckv.h. */
+ * its bounds; nothing is read or written out of bounds, and the tokens concerned are left out
+ * (dckv_attention: of a sequence with a bad length or offset; the slots of a bad page count as
+ * zero keys and values).  DCKV_ETIMEOUT as in dckv.h: the call's outputs are undefined. */
 #ifndef DCKV_CACHE_H_
 #define DCKV_CACHE_H_
 
@@ -130,8 +131,8 @@ typedef struct {
  * rotated (forward) on their way, at position positions[token] or, where positions (device
  * int32 [n_tokens]) is NULL, at their slot; without it they are copied.  With q (device
  * [n_tokens][n_q_heads][head_dim], needs rope), q is rotated at the same position into q_out,
- * which may be q itself with its strides, or must not overlap it.  Two tokens of one call must
- * not share a slot.  With n_b = kv_lens[b] and no rope this takes over what dckv_decode wrote:
+ * which may be q itself with its strides, or must not overlap it.  k, v and q must not overlap
+ * the pools, and two tokens of one call must not share a slot.  With n_b = kv_lens[b] and no rope this takes over what dckv_decode wrote:
  * layer stride n_tokens * 512, token stride 512, head stride 256. */
 typedef struct {
   const void *k, *v;
@@ -184,8 +185,9 @@ typedef struct {
 } dckv_attention_args;
 
 /* Workspace bytes for dckv_attention on this pool, batch and head count (0 on bad arguments).
- * It depends on max_new, not on the lengths.  Its contents need no preparation; calls that may
- * overlap in time (two streams, two graphs) need one each. */
+ * It depends on max_new, not on the lengths: up to 5 MB while max_new * g <= 16, up to 43 MB
+ * above that.  256-byte aligned; its contents need no preparation; calls that may overlap in time
+ * (two streams, two graphs) need one each. */
 size_t dckv_attention_workspace_bytes(const dckv_kv_pool *pool, const dckv_cache_batch *batch, int n_q_heads);
 
 int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *batch, const dckv_attention_args *args,

@@ -809,8 +809,11 @@ struct PairAttn {
   static constexpr int AREA = 512 + 2048;  // barriers; exchange, before that the plan
   static constexpr int FIT = (232448 - AREA - Q_BYTES) / BUF_BYTES;
   static constexpr int STAGES = FIT > 10 ? 10 : FIT;
-  static constexpr int SMEM = Q_BYTES + STAGES * BUF_BYTES + AREA;
-  static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory");
+  // All of the SM's shared memory, used or not: no second block that holds TMEM may share the SM.  Two
+  // pairs of different kernels, each holding the TMEM of one SM and waiting for the other's, would
+  // wait for ever.
+  static constexpr int SMEM = 232448;
+  static_assert(STAGES >= 4 && Q_BYTES + STAGES * BUF_BYTES + AREA <= SMEM, "shared memory");
 };
 
 template <int STAGES>

@@ -354,6 +354,48 @@ def test_attention_many_tiles_per_block(dim, dtype, group, page):
     check_attention(c, [1] * 7, 4 * group)
 
 
+@pytest.mark.parametrize("count", [33, 400])
+@pytest.mark.parametrize("dim,group,new", [(64, 4, 1), (128, 3, 9), (64, 40, 1)])
+def test_attention_many_sequences(count, dim, group, new):
+    """More units than a warp or a block has lanes to count them; sequences without new tokens or
+    slots among them."""
+    r = np.random.RandomState(count)
+    lens = r.randint(0, 90, count).tolist()
+    news = [int(r.randint(0, new + 1)) for _ in range(count)]
+    c = Paged(58, lens, 1, 1, dim, 16)
+    check_attention(c, news, group, max_new=new, pad=1)
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_attention_more_heads_than_rows(new):
+    """200 query heads on one KV head: more than a row tile holds."""
+    c = Paged(59, [300, 40], 1, 1, 128, 32)
+    check_attention(c, [new, new], 200)
+
+
+def test_cache_beyond_32_bits():
+    """Pages whose offsets pass 2^32 bytes and 2^31 elements: append, attention and rows."""
+    pages, rows, dim = 300_000, 16, 256
+    k = torch.empty(1, pages, rows, 2, dim, dtype=BF16, device="cuda")
+    v = torch.empty_like(k)
+    c = Paged.__new__(Paged)
+    c.__dict__.update(lens=[40, 70], page=rows, layers=1, heads=2, dim=dim, dtype=BF16, k=k, v=v, pool=D.kv_pool(k, v),
+                      tables=[[pages - 1, 3, pages - 7], [pages - 2, pages // 2, pages - 3, 0, pages - 4]])
+    new_k, new_v, st = normal(1, 1, 110, 2, dim), normal(2, 1, 110, 2, dim), status()
+    D.dckv_cache_append(c.pool, c.batch([40, 70]), new_k, new_v, st)
+    at = 0
+    for table, n in zip(c.tables, c.lens):
+        p, r = [t.cuda() for t in OC.slots(table, n, rows)]
+        assert torch.equal(k[0, p, r], new_k[0, at: at + n]) and torch.equal(v[0, p, r], new_v[0, at: at + n])
+        at += n
+    check_attention(c, [1, 1], 8)
+    check_attention(c, [40, 33], 8)
+    out = torch.empty(110, 2 * 2 * dim, dtype=BF16, device="cuda")
+    D.dckv_cache_rows(c.pool, c.batch([40, 70]), out, st)
+    assert int(st) == 0
+    assert torch.equal(out.view(110, 2, 2, dim), torch.stack([new_k[0], new_v[0]], 1))
+
+
 @pytest.mark.parametrize("dim,new", [(256, 1), (128, 40), (256, 200)])
 def test_attention_large_scores(dim, new):
     """Scores far beyond exp's range (the running maximum moves, weights underflow)."""
@@ -406,6 +448,26 @@ def test_attention_repeats_bit_for_bit(new):
     for _ in range(3):
         _, o2, l2 = attend(c, news, 8, q=q)
         assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dim,new,other", [(64, 40, 64), (64, 40, 1), (256, 20, 30)])
+def test_attention_overlapping_calls(dim, new, other):
+    """Two calls in flight on two streams over and over: each gives what it gives alone."""
+    c = Paged(83, [700, 900, 333], 1, 2, dim, 32)
+    jobs = []
+    for n, seed in ((new, 1), (other, 2)):
+        q = normal(seed, 3 * n, 8, dim)
+        bt = c.batch([n] * 3)
+        _, want, _ = attend(c, [n] * 3, 8, q=q)
+        ws = torch.empty(D.dckv_attention_workspace_bytes(c.pool, bt, 8), dtype=torch.uint8, device="cuda")
+        jobs.append((bt, q, want, torch.empty_like(want), status(), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for bt, q, _, got, st, ws, s in jobs:
+            D.dckv_attention(c.pool, 0, bt, q, got, st, ws, stream=s)
+    torch.cuda.synchronize()
+    for _, _, want, got, st, _, _ in jobs:
+        assert torch.equal(want, got) and int(st) == 0
 
 
 @pytest.mark.parametrize("new", [1, 40])
