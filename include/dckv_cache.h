@@ -185,8 +185,8 @@ typedef struct {
 } dckv_attention_args;
 
 /* Workspace bytes for dckv_attention on this pool, batch and head count (0 on bad arguments).
- * It depends on max_new, not on the lengths: up to 5 MB while max_new * g <= 16, up to 43 MB
- * above that.  256-byte aligned; its contents need no preparation; calls that may overlap in time
+ * It depends on max_new, not on the lengths: up to 3 MB where max_new * g is small (8, or 16
+ * below dim 256), else up to 43 MB.  256-byte aligned; its contents need no preparation; calls that may overlap in time
  * (two streams, two graphs) need one each. */
 size_t dckv_attention_workspace_bytes(const dckv_kv_pool *pool, const dckv_cache_batch *batch, int n_q_heads);
 

@@ -115,10 +115,11 @@ __device__ __forceinline__ bool walk_next(AttnWalk &w, const BatchDev &bt, const
 }
 
 // How the line is cut.  By default into equal pieces, wherever they begin and end (stream): no
-// block waits for another, but a block may pass from unit to unit, which costs it the time of
-// PLAN_STEPS tiles or so (the old unit's join or output, the new unit's Q).  Where every unit can
-// be cut into equal parts of at most T tiles, one part per block, with T no more than that above
-// the stream's piece, the parts win (parts).
+// block waits for another, but a block may pass from unit to unit, which costs it the time of some
+// tiles (the old unit's join or output, the new unit's Q).  Where every unit can be cut into equal
+// parts of at most T tiles, one part per block, with T at most PLAN_TRIES - 1 steps (a tile, or a
+// thirty-second of the piece) above the stream's piece, the parts win: five short ragged chunks took
+// 37 us as a stream, 23 us in parts (with the chained launches of the same change).
 constexpr int PLAN_TRIES = 4;
 
 struct AttnPlanSmem {
@@ -151,7 +152,7 @@ __device__ __forceinline__ int last_worker(const AttnPlan &pl, const AttnWalk &w
   return (int)div_wide(end * pl.workers + pl.line - 1, pl.line) - 1;
 }
 
-// Worker c's part number k of its unit's n (parts), or its piece from tile `off` of its unit on.
+// Part number k of the walk's unit.
 __device__ __forceinline__ void walk_part(AttnWalk &w, const AttnPlan &pl, const BatchDev &bt, const AttnDev &a,
                                           const AttnShape &sh, int k) {
   w.t0 = 0;
@@ -327,13 +328,7 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
     }
     __syncthreads();
     w.unit = sm->unit;
-    w.t0 = 0;
-    w.left = 0x7fffffff;
-    walk_load(w, bt, a, sh);
-    const int n = (w.tiles + pl.part - 1) / pl.part, k = sm->off;
-    w.t0 = (int)((int64_t)w.tiles * k / n);
-    w.t1 = (int)((int64_t)w.tiles * (k + 1) / n);
-    w.left = w.t1 - w.t0;
+    walk_part(w, pl, bt, a, sh, sm->off);
     return true;
   }
   if (c >= pl.workers) return false;
@@ -461,7 +456,7 @@ __device__ __forceinline__ void store4(T *dst, float4 v) {
 }
 
 // ------------------------------------------------------------------ few rows: one warp, 16 keys
-// Rows 8 NT at most (single tokens of up to 16 query heads per KV head).  Every K and V byte is
+// Rows 8 NT at most (single tokens of up to 8 or 16 query heads per KV head).  Every K and V byte is
 // used for 8 or 16 rows only, so HBM bounds it; the kernel's shape keeps as many loads in flight
 // as shared memory holds and no barrier in the loop.  Each of four warps runs its own ring of
 // stages (a slice of 16 keys: K and V, fetched by TMA with the 128-byte swizzle) and its own
@@ -515,6 +510,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
     }
     fence_mbar_init();
   }
+  __syncthreads();  // the abort flag is set
   asm volatile("griddepcontrol.wait;" ::: "memory");
   AttnPlan pl;
   AttnWalk w;
@@ -778,11 +774,11 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
 }
 
 // ------------------------------------------------------------------ many rows: CTA pairs
-// More than 16 packed rows: tcgen05 with cta_group::2.  A pair takes 256 rows (128 per CTA) and
+// More than 8 (dim 256) or 16 packed rows: tcgen05 with cta_group::2.  A pair takes 256 rows (128 per CTA) and
 // walks key tiles of 128: S = Q K^T (M 256, N 128) and O += P V (M 256, N dim), each CTA holding
 // half of K (64 keys, all dims) and half of V (all keys, half the dims).  A CTA alone would
-// stream a whole K and V tile per 128 rows, 128 bytes per clock at the tensor rate and dim 256;
-// the pair needs half of that per SM, what L2 gives.
+// stream a whole K and V tile per 128 rows, 64 bytes per clock at the tensor rate and dim 256, all
+// that L2 gives an SM; the pair needs half of that.
 // TMEM (512 columns): O in the first `dim`, then two S tiles of 128 columns; P overwrites the
 // first half of its own S tile as 16-bit pairs and is the A operand of the second product.  (One S
 // tile, freed once it is in registers, and two P tiles of their own measured the same.)
@@ -1439,12 +1435,16 @@ static AttnLayout attn_layout(int rows, int dim) {  // rows: 8, 16 or PAIR_ROWS
   return l;
 }
 
-// Rows of a tile: 8 or 16 where every sequence's packed rows fit (k_attend_few), else a pair's
-// 256 (k_attend_many).  A group of more than 128 heads does not fit a CTA's rows and takes tiles
-// of 16, several per token.
-static int attn_rows(const BatchDev &b, int group) {
+// Rows of a tile: 8 or, below dim 256, 16 where every sequence's packed rows fit (k_attend_few),
+// else a pair's 256 (k_attend_many).  Measured on 64 ragged sequences of up to 8,192 slots, few / many:
+// dim 256, 8 rows 117 / 133 us, 16 rows 160 / 135; dim 128, 8 rows 75 / 112, 16 rows 88 / 110, 24 rows
+// (two tiles of 16 at dim 256: 200) many 106; dim 64, 16 rows 72 / 106.  One sequence of 1,000 slots:
+// the same within 1 us.  A group of more than 128 heads does not fit a CTA's rows and takes the few
+// rows' tiles, several per token.
+static int attn_rows(const BatchDev &b, int group, int dim) {
   const int64_t rows = (int64_t)b.max_new * group;
-  return rows <= 8 ? 8 : rows <= 16 || group > 128 ? 16 : PAIR_ROWS;
+  const int few = dim < 256 ? 16 : 8;
+  return rows <= 8 ? 8 : rows <= few || group > 128 ? few : PAIR_ROWS;
 }
 
 // Q as [tokens][heads][dim]; box: 64 dims x a group's heads x the tokens of one CTA's tile.
@@ -1471,7 +1471,7 @@ extern "C" size_t dckv_attention_workspace_bytes(const dckv_kv_pool *pool, const
     fail(DCKV_EINVAL, "n_q_heads %d is not a multiple of the pool's heads", n_q_heads);
     return 0;
   }
-  return attn_layout(attn_rows(b, n_q_heads / p.heads), p.dim).total;
+  return attn_layout(attn_rows(b, n_q_heads / p.heads, p.dim), p.dim).total;
 }
 
 static int sm_count(int device, int &n) {
@@ -1546,7 +1546,8 @@ template <typename T, int D>
 static int run_attend(const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mq, const PoolDev &p, const BatchDev &b,
                       const AttnDev &a, const AttnShape &sh, const PairMaps &mp, int device, cudaStream_t st) {
   if (sh.rows == 8) return run_attend_few<T, D, 1>(mk, mv, p, b, a, sh, device, st);
-  if (sh.rows == 16) return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, device, st);
+  if constexpr (D < 256)
+    if (sh.rows == 16) return run_attend_few<T, D, 2>(mk, mv, p, b, a, sh, device, st);
   return run_attend_many<T, D>(mk, mv, mq, p, b, a, sh, mp, device, st);
 }
 
@@ -1585,7 +1586,7 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
     return fail(DCKV_EINVAL, "out overlaps q");
   const int group = hq / p.heads;
   AttnShape sh;
-  const int slot_rows = attn_rows(b, group);  // of the workspace's parts
+  const int slot_rows = attn_rows(b, group, p.dim);  // of the workspace's parts
   const bool many = slot_rows == PAIR_ROWS;
   const int cta_tokens = many ? 128 / group : 0;
   sh.rows = many ? 2 * cta_tokens * group : slot_rows;
