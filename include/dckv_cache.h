@@ -58,8 +58,8 @@ extern "C" {
                                    the gradient of x from the gradient of the output       */
 #define DCKV_ROPE_INVERSE 2     /* its inverse: the transpose with 1 / m in place of m     */
 
-/* A rotation: angle of pair i at position p = p * freq[i] radians (the product and its
- * reduction modulo 2 pi in fp64), cos and sin in fp32, times `magnitude` m.  Dims past
+/* A rotation: angle of pair i at position p = p * freq[i] radians (multiplied and reduced to
+ * within a turn in fp64), cos and sin in fp32, times `magnitude` m.  Dims past
  * rotary_dim are not rotated.  Filled by dckv_rope_init, or by the caller. */
 typedef struct {
   int32_t rotary_dim; /* even, 2 .. 2 * DCKV_ROPE_MAX_PAIRS                                */

@@ -5,7 +5,7 @@
 // All three move each element once and do 3 flops on it at most, so HBM bounds them on long
 // inputs and the launch and a chain of dependent loads bound them on short ones.  A block takes one
 // token: it looks its slot up and computes its (cos, sin) pairs once, into shared memory, and every
-// head (and layer) reads them from there -- the fp64 reduction and sincosf cost about as much as
+// head (and layer) reads them from there -- the angles cost about as much as
 // the whole copy if each head repeats them.  Elements move as 16-byte vectors: a "chunk" is two
 // vectors, the two halves of V pairs (half layout) or V whole pairs (interleaved layout).
 // Blocks are small (128 threads) where there are many, so that some blocks' loads cover others'
@@ -29,7 +29,7 @@ struct RopeDev {
   int r = 0;  // rotary_dim; 0: copy
   int interleaved = 0;
   float mc = 1.f, ms = 1.f;
-  double freq[DCKV_ROPE_MAX_PAIRS] = {};
+  double turns[DCKV_ROPE_MAX_PAIRS] = {};  // freq / (2 pi): turns per position
 };
 
 // Division of n < 2^31 by a divisor known on the host, as a multiplication: with s = ceil(log2 d)
@@ -143,11 +143,13 @@ __device__ __forceinline__ void rotate_chunk(Vec<T, V> &x0, Vec<T, V> &x1, const
   }
 }
 
-// One pair's (cos, sin) of the token at position pos, the same angle reduction as the decoder's
-// RoPE, scaled as the mode asks.
+// One pair's (cos, sin) of the token at position pos, scaled as the mode asks.  The angle is counted
+// in turns, in fp64, and its whole turns dropped there, which leaves an argument for sincospif that
+// fp32 holds to 2^-25 turns or better.
 __device__ __forceinline__ float2 rope_pair(const RopeDev &rope, int pos, int i) {
+  const double t = (double)pos * rope.turns[i];
   float c, s;
-  rope_cs(pos, i, rope.freq, c, s);
+  sincospif((float)(2.0 * (t - rint(t))), &s, &c);
   return make_float2(c * rope.mc, s * rope.ms);
 }
 
@@ -345,7 +347,7 @@ static int check_spec(const dckv_rope_spec *s, int mode, RopeDev &d) {
     return fail(DCKV_EINVAL, "rotary magnitude must be finite and positive");
   for (int i = 0; i < s->rotary_dim / 2; ++i) {
     if (!std::isfinite(s->freq[i])) return fail(DCKV_EINVAL, "rotary frequency %d is not finite", i);
-    d.freq[i] = s->freq[i];
+    d.turns[i] = s->freq[i] * 0.15915494309189535;  // 1 / (2 pi)
   }
   d.r = s->rotary_dim;
   d.interleaved = s->layout == DCKV_ROPE_INTERLEAVED;

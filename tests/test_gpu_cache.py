@@ -4,9 +4,9 @@
 Tolerances, from arithmetic (u(t) = finfo(t).eps / 2, half a step relative):
   rotation   |out| u(t) for the one rounding, plus (|a| + |b|) m 8e-7 for fp32 arithmetic: the
              reduced angle's rounding to fp32 (pi 2^-24 = 1.9e-7), its fp64 product and reduction
-             (|angle| 2^-52, 4.8e-7 at 2^31 radians, below 1e-9 under 10^6), sincosf (2 ulp, 1.2e-7)
-             and the two products and their sum and the magnitude's product (4 roundings, 2.4e-7
-             of |a| + |b|); the sums stay below 8e-7 for positions up to 2^28.
+             (|angle| 2^-52, 4.8e-7 at 2^31 radians, below 1e-9 under 10^6), cos and sin (2 ulp,
+             1.2e-7) and the two products and their sum and the magnitude's product (4 roundings,
+             2.4e-7 of |a| + |b|); the sums stay below 8e-7 for positions up to 2^28.
   attention  a score's error ds: dim products summed in fp32, each partial sum at most reach =
              scale sum |q||k|, truncated or rounded by 2^-23 of it, and a few products and
              subtractions of numbers up to 2 reach: ds = reach (dim + 8) 2^-23.  A weight is off by
