@@ -614,8 +614,8 @@ def dckv_attention(pool, layer, batch, q, out, status, workspace, scale=None, ca
     n = shape[0]
     if n == 0:
         return out
-    a = _AttentionArgs(q.data_ptr(), out.data_ptr(), lp, qs[0], qs[1], os_[0], os_[1], n, shape[1], layer,
-                       1 if causal else 0, pool.dim ** -0.5 if scale is None else scale)
+    a = _AttentionArgs(q.data_ptr(), out.data_ptr(), lp, qs[0], qs[1], os_[0], os_[1], n, shape[1], int(layer),
+                       1 if causal else 0, pool.dim ** -0.5 if scale is None else float(scale))
     r = lib().dckv_attention(pool.ref, batch.ref, ctypes.byref(a), st, workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _device_stream(dev, stream))
     if r:

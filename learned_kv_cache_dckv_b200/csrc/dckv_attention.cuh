@@ -1595,7 +1595,7 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   const int64_t most_rows = std::min<int64_t>(b.max_new, std::max<int64_t>(n, 1)) * group;
   if (most_rows > 0x7fffffffll - PAIR_ROWS) return fail(DCKV_EINVAL, "max_new times the head group is too large");
   const int64_t row_tiles = (most_rows + sh.rows - 1) / sh.rows;
-  if (row_tiles * b.batch > 0x7fffffffll) return fail(DCKV_EINVAL, "batch times max_new is too large");
+  if (row_tiles * b.batch > 1ll << 30) return fail(DCKV_EINVAL, "batch times max_new is too large");
   sh.row_tiles = (int)row_tiles;
   sh.unit_div = FastDiv((uint32_t)row_tiles);
   sh.units = (int)(row_tiles * b.batch);
