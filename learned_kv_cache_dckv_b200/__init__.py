@@ -418,7 +418,7 @@ def _on(device, name, t):
 def _int32_on(device, name, t):
     if t.get_device() != device or device < 0:
         _bad(f"{name} is on {t.device}, not on cuda:{max(device, 0)}")
-    if _dtype_code(t) != "int32":
+    if _CODES.get(t.dtype) != "int32" and _dtype_code(t) != "int32":
         _bad(f"{name} must be int32, not {t.dtype}")
     if not t.is_contiguous():
         _bad(f"{name} must be contiguous")
@@ -460,7 +460,7 @@ def dckv_rope(spec, x, positions, out, mode="forward", stream=None):
     """Rotates x [n, heads, dim] (bf16, fp16 or fp32) by positions int32 [n] into out (which may
     be x).  mode "forward", "gradient" (the transpose) or "inverse"."""
     shape = x.shape
-    if len(shape) != 3 or out.shape != shape or positions.shape != shape[:1]:
+    if len(shape) != 3 or out.shape != shape or positions.dim() != 1 or len(positions) != shape[0]:
         _bad("x and out must be [n, heads, dim] alike and positions [n]")
     code = _dtype_code(x)
     if out.dtype != x.dtype or code == "int32":

@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
     fence_mbar_init();
   }
   __syncthreads();  // the abort flag is set
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_chained();
   AttnPlan pl;
   AttnWalk w;
   const int c = blockIdx.x;
@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_arrive();  // both CTAs' barriers are initialised before any cross-CTA signal
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_chained();
   AttnPlan pl;
   AttnWalk w;
   const bool any = attn_plan<PAIR_THREADS>(bt, a, sh, PLAN_TRIES, c, plan_sm, pl, w);
@@ -1228,7 +1228,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_few(const AttnDev a, int 
   constexpr int V = E >= 4 ? 4 : E;
   __shared__ float acc_sm[JOIN_WARPS][D];
   __shared__ float2 ml_sm[JOIN_WARPS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are still written
+  wait_chained();  // launched while the parts are still written
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 ds = a.desc[2 * c];
   if (ds.x < 0) return;
@@ -1365,7 +1365,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_many(const AttnDev a, int
   constexpr int CHUNKS = D / 16 / JOIN_STEPS;
   __shared__ float4 acc_sm[JOIN_WARPS][JOIN_STEPS][32];
   __shared__ float2 ml_sm[JOIN_WARPS][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are still written
+  wait_chained();  // launched while the parts are still written
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 3;
   const int4 ds = a.desc[2 * c];
   if (ds.x < 0) return;
@@ -1489,29 +1489,6 @@ static int allow_smem(const void *kern, int smem, int device, std::atomic<uint64
   if (done.load() >> device & 1) return DCKV_OK;
   CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   done.fetch_or(1ull << device);
-  return DCKV_OK;
-}
-
-// Launches with programmatic stream serialisation: a kernel's blocks are set up while the kernel
-// before it in the stream ends, and wait for it (griddepcontrol.wait) before they read or write
-// global memory.
-static int launch_chained(const void *kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, void **args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  CK(cudaLaunchKernelExC(&cfg, kern, args));
-  ++g_launches;
   return DCKV_OK;
 }
 

