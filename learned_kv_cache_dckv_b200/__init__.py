@@ -407,10 +407,10 @@ def _dtype_code(t):
 def _on(device, name, t):
     """t's strides, having checked that it sits on that CUDA device and that its last dimension is
     contiguous."""
+    st = t.stride()
     if t.get_device() != device or device < 0:
         _bad(f"{name} is on {t.device}, not on cuda:{max(device, 0)}")
-    st = t.stride()
-    if st and st[-1] != 1 and t.shape[-1] > 1:
+    if st[-1] != 1 and t.shape[-1] > 1:
         _bad(f"the last dimension of {name} must be contiguous")
     return st
 
@@ -462,8 +462,11 @@ def dckv_rope(spec, x, positions, out, mode="forward", stream=None):
     shape = x.shape
     if len(shape) != 3 or out.shape != shape or positions.dim() != 1 or len(positions) != shape[0]:
         _bad("x and out must be [n, heads, dim] alike and positions [n]")
-    code = _dtype_code(x)
-    if out.dtype != x.dtype or code == "int32":
+    dt = x.dtype
+    code = _CODES.get(dt)
+    if code is None:
+        code = _dtype_code(x)
+    if out.dtype is not dt or code == "int32":
         _bad("x and out must have one type, bf16, fp16 or fp32")
     m = ROPE_MODES.get(mode)
     if m is None:
@@ -495,7 +498,7 @@ def kv_pool(k, v) -> KvPool:
     p = KvPool(k.data_ptr(), v.data_ptr(), dev, code, L, heads, dim, rows, pages, *ks[:4], *vs[:4])
     p.tensors = (k, v)
     # what the calls below compare with (a ctypes field is slower to read)
-    p.dev, p.code, p.kv_shape, p.dim, p.ref = dev, code, (L, heads, dim), dim, ctypes.byref(p)
+    p.dev, p.dt, p.kv_shape, p.dim, p.ref = dev, k.dtype, (L, heads, dim), dim, ctypes.byref(p)
     return p
 
 
@@ -528,12 +531,14 @@ def dckv_cache_append(pool, batch, k, v, status, rope=None, positions=None, q=No
     by `rope` if given; q [n, q heads, dim] rotated into q_out beside them."""
     if k.dim() == 3:
         k, v = k[None], v[None]
-    shape, dev, code = k.shape, pool.dev, pool.code
-    if len(shape) != 4 or (shape[0], shape[2], shape[3]) != pool.kv_shape or v.shape != shape:
+    shape, dev, dt = k.shape, pool.dev, pool.dt
+    if len(shape) != 4 or v.shape != shape:
         _bad("k and v must be [layers, n, heads, dim] of the pool")
-    if _dtype_code(k) != code or v.dtype != k.dtype:
+    layers, n, heads, dim = shape
+    if (layers, heads, dim) != pool.kv_shape:
+        _bad("k and v must be [layers, n, heads, dim] of the pool")
+    if k.dtype is not dt or v.dtype is not dt:
         _bad("k and v must have the pool's type")
-    n = shape[1]
     st = _same_device(pool, batch, status)
     ks, vs = _on(dev, "k", k), _on(dev, "v", v)
     qp = op = pos = None
@@ -541,11 +546,14 @@ def dckv_cache_append(pool, batch, k, v, status, rope=None, positions=None, q=No
     hq = 0
     if q is not None:
         qshape = q.shape
-        if q_out is None or len(qshape) != 3 or qshape[0] != n or qshape[2] != pool.dim or q_out.shape != qshape:
+        if q_out is None or len(qshape) != 3 or q_out.shape != qshape:
             _bad("q and q_out must be [n, q heads, dim]")
-        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+        nq, hq, dq = qshape
+        if nq != n or dq != dim:
+            _bad("q and q_out must be [n, q heads, dim]")
+        if q.dtype is not dt or q_out.dtype is not dt:
             _bad("q and q_out must have the pool's type")
-        qs, os_, hq = _on(dev, "q", q), _on(dev, "q_out", q_out), qshape[1]
+        qs, os_ = _on(dev, "q", q), _on(dev, "q_out", q_out)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         _bad("q_out without q")
@@ -569,7 +577,7 @@ def dckv_cache_rows(pool, batch, rows, status, rope=None, positions=None, stream
     L, H, dim = pool.kv_shape
     if rows.dim() != 2 or rows.shape[1] != 2 * L * H * dim:
         _bad("rows must be [n, layers * 2 * heads * dim]")
-    if _dtype_code(rows) != pool.code:
+    if rows.dtype is not pool.dt:
         _bad("rows must have the pool's type")
     st = _same_device(pool, batch, status)
     rs = _on(pool.dev, "rows", rows)
@@ -597,10 +605,13 @@ def dckv_attention_workspace_bytes(pool, batch, n_q_heads) -> int:
 def dckv_attention(pool, layer, batch, q, out, status, workspace, scale=None, causal=True, lse=None, stream=None):
     """Attention of q [n, q heads, dim] over the sequences' slots in `layer` into out (same shape)
     and, if given, lse fp32 [n, q heads].  scale: dim ** -0.5 unless given."""
-    shape, dev = q.shape, pool.dev
-    if len(shape) != 3 or shape[2] != pool.dim or out.shape != shape:
+    shape, dev, dt = q.shape, pool.dev, pool.dt
+    if len(shape) != 3 or out.shape != shape:
         _bad("q and out must be [n, q heads, dim]")
-    if _dtype_code(q) != pool.code or out.dtype != q.dtype:
+    n, hq, dim = shape
+    if dim != pool.dim:
+        _bad("q and out must be [n, q heads, dim] of the pool")
+    if q.dtype is not dt or out.dtype is not dt:
         _bad("q and out must have the pool's type")
     st = _same_device(pool, batch, status)
     qs, os_ = _on(dev, "q", q), _on(dev, "out", out)
@@ -608,14 +619,14 @@ def dckv_attention(pool, layer, batch, q, out, status, workspace, scale=None, ca
         _bad("the workspace must be contiguous, on the pool's device")
     lp = None
     if lse is not None:
-        if lse.shape != shape[:2] or _dtype_code(lse) != DCKV_FP32 or lse.get_device() != dev or not lse.is_contiguous():
+        if lse.shape != shape[:2] or _dtype_code(lse) != DCKV_FP32 or lse.get_device() != dev or \
+                not lse.is_contiguous():
             _bad("lse must be contiguous fp32 [n, q heads] on the pool's device")
         lp = lse.data_ptr()
-    n = shape[0]
     if n == 0:
         return out
-    a = _AttentionArgs(q.data_ptr(), out.data_ptr(), lp, qs[0], qs[1], os_[0], os_[1], n, shape[1], int(layer),
-                       1 if causal else 0, pool.dim ** -0.5 if scale is None else float(scale))
+    a = _AttentionArgs(q.data_ptr(), out.data_ptr(), lp, qs[0], qs[1], os_[0], os_[1], n, hq, int(layer),
+                       1 if causal else 0, dim ** -0.5 if scale is None else float(scale))
     r = lib().dckv_attention(pool.ref, batch.ref, ctypes.byref(a), st, workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _device_stream(dev, stream))
     if r:
