@@ -572,6 +572,53 @@ def test_step_in_a_graph(new):
     expect(steps[0], now)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("new", [1, 40])
+def test_inputs_from_another_stream(new, captured):
+    """Queries, keys and values come late from another stream, by events, and the outputs go back to
+    it; eager and in a captured graph that forks and joins.  The calls' chained launches must wait."""
+    c = Paged(117, [900, 300], 1, 2, 128, 32)
+    spec, n, hq = D.rope_spec(128), 2 * new, 8
+    bt, st = c.batch([new, new]), status()
+    ws = torch.empty(D.dckv_attention_workspace_bytes(c.pool, bt, hq), dtype=torch.uint8, device="cuda")
+    fresh = normal(5, n, hq + 4, 128)
+    x, q = torch.zeros_like(fresh), torch.zeros(n, hq, 128, device="cuda", dtype=BF16)
+    out, copy = torch.zeros_like(q), torch.zeros_like(q)
+    where = torch.cat([torch.arange(900 - new, 900), torch.arange(300 - new, 300)]).int().cuda()
+    load = torch.randn(2048, 2048, device="cuda")
+    side = torch.cuda.Stream()
+
+    def work():
+        y = load
+        for _ in range(20):  # some milliseconds before the inputs are there
+            y = (y @ load).clamp_(-1, 1)
+        x.copy_(fresh + 0 * y[0, 0].to(BF16))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            D.dckv_cache_append(c.pool, bt, x[:, hq: hq + 2], x[:, hq + 2:], st, rope=spec, q=x[:, :hq], q_out=q)
+            D.dckv_attention(c.pool, 0, bt, q, out, st, ws)
+        torch.cuda.current_stream().wait_stream(side)
+        copy.copy_(out)
+
+    work()
+    torch.cuda.synchronize()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            work()
+    for i in range(3):
+        fresh.copy_(normal(20 + i, n, hq + 4, 128))
+        x.fill_(float("nan"))
+        out.fill_(float("nan"))
+        g.replay() if captured else work()
+        torch.cuda.synchronize()
+        q2 = torch.empty_like(q)
+        D.dckv_rope(spec, fresh[:, :hq], where, q2)
+        assert torch.equal(q, q2)
+        _, out2, _ = attend(c, [new, new], hq, q=q2)
+        assert torch.equal(copy, out2) and int(st) == 0
+
+
 def test_two_streams_at_once():
     """Two calls in flight on two streams, each with its own workspace."""
     c = Paged(113, [3000, 2500], 1, 2, 256, 64)
