@@ -285,7 +285,10 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
     for (int u = u0; u < u1; ++u) {
       const int t = per == 1 ? one : tiles_of(u);
 #pragma unroll
-      for (int j = 0; j < PLAN_TRIES; ++j) cnt[j] += (int)((uint32_t)(t + (int)base + j * step - 1) / (uint32_t)((int)base + j * step));
+      for (int j = 0; j < PLAN_TRIES; ++j) {
+        const uint32_t part = (uint32_t)base + j * step;
+        cnt[j] += (int)((t + part - 1) / part);
+      }
     }
 #pragma unroll
     for (int j = 0; j < PLAN_TRIES; ++j) {
@@ -836,7 +839,8 @@ struct PairMaps {
 template <typename T, int D>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
     k_attend_many(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_q, const PoolDev p, const BatchDev bt, const AttnDev a, const AttnShape sh, const PairMaps mp) {
+                  const __grid_constant__ CUtensorMap tm_q, const PoolDev p, const BatchDev bt, const AttnDev a,
+                  const AttnShape sh, const PairMaps mp) {
   using C = PairAttn<D>;
   constexpr int STAGES = C::STAGES;
   constexpr uint32_t S_COL = 256;
@@ -1416,7 +1420,8 @@ static int map_pages(CUtensorMap *m, const void *ptr, bool bf16, const PoolDev &
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  box_dims == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  box_dims == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DCKV_ECUDA, "tensor map (pages) encode failed: %d", (int)r);
   return DCKV_OK;
 }
@@ -1586,7 +1591,8 @@ extern "C" int dckv_attention(const dckv_kv_pool *pool, const dckv_cache_batch *
   RET(sm_count(pool->device, sms));
   char *ws = (char *)workspace;
   const AttnDev a{(const char *)args->q, (char *)args->out, args->lse, qt, qh, ot, oh, hq, group, args->causal,
-                  FastDiv((uint32_t)group), args->scale * 1.4426950408889634f, status, (float4 *)(ws + lay.part_o), (float2 *)(ws + lay.part_ml),
+                  FastDiv((uint32_t)group), args->scale * 1.4426950408889634f, status, (float4 *)(ws + lay.part_o),
+                  (float2 *)(ws + lay.part_ml),
                   (int4 *)(ws + lay.desc),
                   many ? std::min(sms / 2, ATTN_MAX_PAIRS) : std::min(sms, ATTN_MAX_WORKERS)};
   const bool bf = pool->dtype == DCKV_BF16;

@@ -5,9 +5,9 @@
 // All three move each element once and do 3 flops on it at most, so HBM bounds them on long
 // inputs and the launch and a chain of dependent loads bound them on short ones.  A block takes one
 // token: it looks its slot up and computes its (cos, sin) pairs once, into shared memory, and every
-// head (and layer) reads them from there -- the angles cost about as much as
-// the whole copy if each head repeats them.  Elements move as 16-byte vectors: a "chunk" is two
-// vectors, the two halves of V pairs (half layout) or V whole pairs (interleaved layout).
+// head (and layer) reads them from there -- the angles cost about as much as the whole copy if each
+// head repeats them.  Elements move as 16-byte vectors: a "chunk" is two vectors, the two halves of V
+// pairs (half layout) or V whole pairs (interleaved layout).
 // Blocks are small (128 threads) where there are many, so that some blocks' loads cover others'
 // look-ups.  Measured on four 4,096-token prompts, six layers, 207 MB (appended without a rotation)
 // and 258 MB (rows): 128 threads 41 and 53 us; 256 threads 45 and 59; a thread per chunk (384) 62
@@ -591,8 +591,9 @@ extern "C" int dckv_cache_append(const dckv_kv_pool *pool, const dckv_cache_batc
   a.head_div = FastDiv((uint32_t)p.heads);
   const unsigned grid = (unsigned)n;
   const int threads = block_threads(n, a.per_token);
-  const void *kern = pool->dtype == DCKV_BF16 ? (vec ? (const void *)k_append<__nv_bfloat16, 8> : (const void *)k_append<__nv_bfloat16, 1>)
-                                              : (vec ? (const void *)k_append<__half, 8> : (const void *)k_append<__half, 1>);
+  const void *bf = vec ? (const void *)k_append<__nv_bfloat16, 8> : (const void *)k_append<__nv_bfloat16, 1>;
+  const void *hf = vec ? (const void *)k_append<__half, 8> : (const void *)k_append<__half, 1>;
+  const void *kern = pool->dtype == DCKV_BF16 ? bf : hf;
   void *kargs[] = {(void *)&r, (void *)&p, (void *)&b, (void *)&a};
   return launch_chained(kern, dim3(grid), threads, 0, 1, st, kargs);
 }
@@ -627,8 +628,9 @@ extern "C" int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch 
   a.status = status;
   const unsigned grid = (unsigned)n_tokens;
   const int threads = block_threads(n_tokens, a.per_token);
-  const void *kern = pool->dtype == DCKV_BF16 ? (vec ? (const void *)k_rows<__nv_bfloat16, 8> : (const void *)k_rows<__nv_bfloat16, 1>)
-                                              : (vec ? (const void *)k_rows<__half, 8> : (const void *)k_rows<__half, 1>);
+  const void *bf = vec ? (const void *)k_rows<__nv_bfloat16, 8> : (const void *)k_rows<__nv_bfloat16, 1>;
+  const void *hf = vec ? (const void *)k_rows<__half, 8> : (const void *)k_rows<__half, 1>;
+  const void *kern = pool->dtype == DCKV_BF16 ? bf : hf;
   void *kargs[] = {(void *)&r, (void *)&p, (void *)&b, (void *)&a};
   return launch_chained(kern, dim3(grid), threads, 0, 1, st, kargs);
 }
