@@ -812,10 +812,19 @@ class PagedCache:
         return dckv_attention(self.pool, layer, batch, q, out, self.status, self._ws, scale=scale, causal=causal,
                               lse=lse)
 
+    def _check_codec(self, codec):
+        """The codec's calls take rows of its own shape and type on trust."""
+        p = self.pool
+        if (p.n_layers, p.n_kv_heads, p.head_dim) != (6, 2, 256) or self.k.dtype != self.torch.bfloat16:
+            _bad("a codec's prompts need a cache of 6 layers, 2 KV heads and 256 dims in bf16")
+        if codec.device != self.device:
+            _bad(f"the codec is on {codec.device}, the cache on {self.device}")
+
     def restore(self, codec, blob, blob_bytes, token_ids, seq_offsets):
         """Decodes a blob's prompts into new sequences of the pages (the decoder rotates the keys
-        as the codec's own rotation does).  Returns the sequences; codec.status has the decoder's
-        status."""
+        as the codec's own rotation does).  The cache must have the codec's layers, heads, dims, type
+        and device.  Returns the sequences; codec.status has the decoder's status."""
+        self._check_codec(codec)
         counts = [int(c) for c in np.diff(np.asarray(seq_offsets, np.int64))]
         if min(counts) < 1:
             _bad("restore takes prompts of at least one token")
@@ -843,7 +852,8 @@ class PagedCache:
 
     def store(self, codec, seqs, token_ids, counts=None):
         """Encodes the sequences' first tokens with a codec: (blob, seq_offsets); codec.blob_size
-        and codec.status as after Codec.encode."""
+        and codec.status as after Codec.encode.  The cache must be one that restore takes."""
+        self._check_codec(codec)
         rows, offsets = self.rows(seqs, counts)
         stream = self.torch.cuda.current_stream(self.device)
         return codec.encode(rows, token_ids, offsets, stream=stream), offsets

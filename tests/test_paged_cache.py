@@ -1,0 +1,116 @@
+"""PagedCache without a GPU: its tensors sit on the host and the library's calls are recorded, so
+nothing here reaches a device.  What the class refuses, and what it keeps when it refuses."""
+import ctypes
+import gc
+import weakref
+
+import numpy as np
+import pytest
+import torch
+
+import learned_kv_cache_dckv_b200 as D
+from learned_kv_cache_dckv_b200 import build as B
+
+HOST = torch.device("cpu")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    B.build()
+    return D.lib()
+
+
+class Codec:
+    """Stands in for D.Codec: counts the calls, gives decoded prompts of zeros."""
+
+    def __init__(self, device=HOST):
+        self.device, self.calls = device, []
+
+    def decode(self, blob, blob_bytes, token_ids, seq_offsets, k_out=None, v_out=None, stream=None):
+        self.calls.append("decode")
+        n = int(np.asarray(seq_offsets)[-1])
+        return [torch.zeros(6, n, 2, 256, dtype=torch.bfloat16) for _ in range(2)]
+
+    def encode(self, rows, token_ids, seq_offsets, blob=None, stream=None):
+        self.calls.append(("encode", tuple(rows.shape), rows.dtype))
+        return torch.zeros(16, dtype=torch.uint8)
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """PagedCache(...) on the host; .calls has the library's calls: (name, arguments, keywords)."""
+    calls = []
+    real = torch.device
+    monkeypatch.setattr(D, "_on", lambda device, name, t: t.stride())
+    monkeypatch.setattr(D, "_int32_on", lambda device, name, t: t.data_ptr())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    for name in ("dckv_cache_append", "dckv_cache_rows", "dckv_attention"):
+        monkeypatch.setattr(D, name, lambda *a, _n=name, **kw: calls.append((_n, a, kw)))
+
+    def make(n_pages=8, page_size=16, **kw):
+        with monkeypatch.context() as m:
+            m.setattr(torch, "device", lambda *a: HOST if a[0] == "cuda" else real(*a))
+            c = D.PagedCache(n_pages, page_size, **kw)
+        c.calls = calls
+        return c
+
+    return make
+
+
+def offsets(*lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+
+
+def tokens(n):
+    return torch.zeros(n, dtype=torch.int32)
+
+
+def keys(cache, n, heads=None):
+    return torch.zeros(cache.pool.n_layers, n, heads or cache.pool.n_kv_heads, cache.pool.head_dim, dtype=cache.k.dtype)
+
+
+def extended(cache, *counts):
+    seqs = [cache.add() for _ in counts]
+    return seqs, cache.extend(seqs, counts)
+
+
+# ------------------------------------------------------------------ the codec's shape and type
+OTHER = [dict(n_layers=1), dict(n_kv_heads=4), dict(head_dim=128), dict(dtype=torch.float16)]
+
+
+@pytest.mark.parametrize("kw", OTHER)
+def test_store_refuses_a_cache_that_is_not_the_codecs(host, kw):
+    """The encoder reads 12,288 bytes per row whatever tensor it is given: rows of another cache
+    would be read out of their bounds."""
+    cache, codec = host(**kw), Codec()
+    seqs, _ = extended(cache, 20)
+    with pytest.raises(D.DckvError) as e:
+        cache.store(codec, seqs, tokens(20))
+    assert e.value.code == D.DCKV_EINVAL and codec.calls == []
+
+
+@pytest.mark.parametrize("kw", OTHER)
+def test_restore_refuses_a_cache_that_is_not_the_codecs(host, kw):
+    cache, codec = host(**kw), Codec()
+    with pytest.raises(D.DckvError) as e:
+        cache.restore(codec, None, 0, tokens(20), offsets(20))
+    assert e.value.code == D.DCKV_EINVAL and codec.calls == []
+    assert len(cache._free) == 8 and cache._len == {}
+
+
+def test_store_and_restore_refuse_another_device(host):
+    cache, codec = host(), Codec(torch.device("meta"))
+    seqs, _ = extended(cache, 20)
+    with pytest.raises(D.DckvError):
+        cache.store(codec, seqs, tokens(20))
+    with pytest.raises(D.DckvError):
+        cache.restore(codec, None, 0, tokens(20), offsets(20))
+    assert codec.calls == []
+
+
+def test_restore_and_store_pass_the_codecs_shape(host):
+    cache, codec = host(), Codec()
+    seqs = cache.restore(codec, None, 0, tokens(53), offsets(20, 33))
+    assert [cache.length(s) for s in seqs] == [20, 33] and len(cache._free) == 8 - 2 - 3
+    _, offs = cache.store(codec, seqs, tokens(53))
+    assert codec.calls == ["decode", ("encode", (53, 6144), torch.bfloat16)] and offs.tolist() == [0, 20, 53]
