@@ -812,20 +812,23 @@ class PagedCache:
         return dckv_attention(self.pool, layer, batch, q, out, self.status, self._ws, scale=scale, causal=causal,
                               lse=lse)
 
-    def _check_codec(self, codec):
-        """The codec's calls take rows of its own shape and type on trust."""
+    def _check_codec(self, codec, token_ids, n_tokens):
+        """The codec's calls take rows of its own shape and type, and the tokens' ids, on trust."""
         p = self.pool
         if (p.n_layers, p.n_kv_heads, p.head_dim) != (6, 2, 256) or self.k.dtype != self.torch.bfloat16:
             _bad("a codec's prompts need a cache of 6 layers, 2 KV heads and 256 dims in bf16")
         if codec.device != self.device:
             _bad(f"the codec is on {codec.device}, the cache on {self.device}")
+        if token_ids is not None and (token_ids.dtype != self.torch.int32 or token_ids.device != self.device or
+                                      not token_ids.is_contiguous() or token_ids.numel() < n_tokens):
+            _bad(f"token ids must be {n_tokens} contiguous int32 on {self.device}")
 
     def restore(self, codec, blob, blob_bytes, token_ids, seq_offsets):
         """Decodes a blob's prompts into new sequences of the pages (the decoder rotates the keys
         as the codec's own rotation does).  The cache must have the codec's layers, heads, dims, type
         and device.  Returns the sequences; codec.status has the decoder's status."""
-        self._check_codec(codec)
         counts = [int(c) for c in np.diff(np.asarray(seq_offsets, np.int64))]
+        self._check_codec(codec, token_ids, sum(counts))
         if min(counts) < 1:
             _bad("restore takes prompts of at least one token")
         stream = self.torch.cuda.current_stream(self.device)
@@ -852,8 +855,10 @@ class PagedCache:
 
     def store(self, codec, seqs, token_ids, counts=None):
         """Encodes the sequences' first tokens with a codec: (blob, seq_offsets); codec.blob_size
-        and codec.status as after Codec.encode.  The cache must be one that restore takes."""
-        self._check_codec(codec)
+        and codec.status as after Codec.encode.  The cache must be one that restore takes; token_ids
+        has an id for each of those tokens (None for a codec that takes none)."""
+        counts = [self._len[s] for s in seqs] if counts is None else [int(c) for c in counts]
+        self._check_codec(codec, token_ids, sum(counts))
         rows, offsets = self.rows(seqs, counts)
         stream = self.torch.cuda.current_stream(self.device)
         return codec.encode(rows, token_ids, offsets, stream=stream), offsets

@@ -114,3 +114,31 @@ def test_restore_and_store_pass_the_codecs_shape(host):
     assert [cache.length(s) for s in seqs] == [20, 33] and len(cache._free) == 8 - 2 - 3
     _, offs = cache.store(codec, seqs, tokens(53))
     assert codec.calls == ["decode", ("encode", (53, 6144), torch.bfloat16)] and offs.tolist() == [0, 20, 53]
+
+
+# ------------------------------------------------------------------ token ids
+BAD_TOKENS = [tokens(19), tokens(20).long(), tokens(40)[::2], torch.zeros(20, dtype=torch.int32, device="meta")]
+
+
+@pytest.mark.parametrize("ids", BAD_TOKENS, ids=["short", "int64", "strided", "elsewhere"])
+def test_restore_and_store_refuse_token_ids_that_do_not_fit(host, ids):
+    """The codec reads one int32 per token from the address that it is given."""
+    cache, codec = host(), Codec()
+    seqs, _ = extended(cache, 20)
+    with pytest.raises(D.DckvError):
+        cache.store(codec, seqs, ids)
+    with pytest.raises(D.DckvError):
+        cache.restore(codec, None, 0, ids, offsets(20))
+    assert codec.calls == [] and len(cache._len) == 1
+
+
+def test_store_counts_every_token_of_a_sequence(host):
+    """Tokens appended behind the prompt count by default: the prompt's ids alone are too few."""
+    cache, codec = host(), Codec()
+    seqs = cache.restore(codec, None, 0, tokens(20), offsets(20))
+    cache.append(cache.extend(seqs, [1]), keys(cache, 1), keys(cache, 1))
+    with pytest.raises(D.DckvError):
+        cache.store(codec, seqs, tokens(20))
+    cache.store(codec, seqs, tokens(20), [20])
+    cache.store(codec, seqs, tokens(21))
+    cache.store(codec, seqs, None)  # a codec without mean models takes none
