@@ -753,6 +753,7 @@ class PagedCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._free = list(range(n_pages - 1, -1, -1))
         self._pages, self._len = {}, {}
+        self._odd = {}  # sequences with keys that are not rotated at their slots: the first such slot
         self._ws = None
         self._next = 0
 
@@ -771,6 +772,7 @@ class PagedCache:
         them in order)."""
         self._free += reversed(self._pages.pop(seq))
         del self._len[seq]
+        self._odd.pop(seq, None)
 
     def _batch(self, seqs, counts):
         torch = self.torch
@@ -781,7 +783,9 @@ class PagedCache:
         offs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
         lens = np.array([self._len[s] for s in seqs], np.int32)
         dev = [torch.from_numpy(a).to(self.device) for a in (offs, lens, table)]
-        return cache_batch(*dev, max(1, max(counts)))
+        batch = cache_batch(*dev, max(1, max(counts)))
+        batch.firsts = {s: self._len[s] - c for s, c in zip(seqs, counts) if c}  # slots of an append's first tokens
+        return batch
 
     def extend(self, seqs, counts) -> CacheBatch:
         """Room for counts[i] more tokens of seqs[i]; the batch of a call that appends them."""
@@ -798,9 +802,16 @@ class PagedCache:
         return self._batch(seqs, counts)
 
     def append(self, batch, k, v, q=None, q_out=None, rotate=True, positions=None):
-        """dckv_cache_append with the cache's rotation (rotate=False: keys come rotated)."""
+        """dckv_cache_append with the cache's rotation (rotate=False: keys come rotated).  Keys that it
+        did not rotate at their slots (rotate=False, or positions given) come back by `rows` and
+        `store` only where these are given positions; a replayed graph is judged by its capture."""
         dckv_cache_append(self.pool, batch, k, v, self.status, rope=self.rope if rotate else None, positions=positions,
                           q=q, q_out=q_out)
+        if not rotate or positions is not None:
+            # a batch that extend did not make does not say whose slots it writes
+            for s, first in getattr(batch, "firsts", dict.fromkeys(self._len, 0)).items():
+                if s in self._len:
+                    self._odd[s] = min(first, self._odd.get(s, first))
 
     def attend(self, layer, batch, q, out=None, scale=None, causal=True, lse=None):
         """dckv_attention on the cache's workspace; out is a new tensor unless given."""
@@ -840,25 +851,31 @@ class PagedCache:
             for s in seqs:
                 self.drop(s)
             raise
-        self.append(batch, k, v, rotate=False)
+        dckv_cache_append(self.pool, batch, k, v, self.status)
         return seqs
 
-    def rows(self, seqs, counts=None):
+    def rows(self, seqs, counts=None, positions=None):
         """The first counts[i] (default: all) tokens of each sequence as pre-RoPE rows, and their
-        offsets: the arguments of Codec.encode."""
+        offsets: the arguments of Codec.encode.  Keys are rotated back from their slots or, if given,
+        from positions (device int32, one per row); a key that `append` did not rotate at its slot
+        needs them."""
         counts = [self._len[s] for s in seqs] if counts is None else [int(c) for c in counts]
+        for s, c in zip(seqs, counts):
+            if positions is None and c > self._odd.get(s, c):
+                _bad(f"keys of sequence {s} are not rotated at their slots from slot {self._odd[s]} on: "
+                     "their rows need positions")
         n = sum(counts)
         rows = self.torch.empty((n, 2 * self.pool.n_layers * self.pool.n_kv_heads * self.pool.head_dim),
                                 dtype=self.k.dtype, device=self.device)
-        dckv_cache_rows(self.pool, self._batch(seqs, counts), rows, self.status, rope=self.rope)
+        dckv_cache_rows(self.pool, self._batch(seqs, counts), rows, self.status, rope=self.rope, positions=positions)
         return rows, np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
 
-    def store(self, codec, seqs, token_ids, counts=None):
+    def store(self, codec, seqs, token_ids, counts=None, positions=None):
         """Encodes the sequences' first tokens with a codec: (blob, seq_offsets); codec.blob_size
         and codec.status as after Codec.encode.  The cache must be one that restore takes; token_ids
-        has an id for each of those tokens (None for a codec that takes none)."""
+        has an id for each of those tokens (None for a codec that takes none); positions as for `rows`."""
         counts = [self._len[s] for s in seqs] if counts is None else [int(c) for c in counts]
         self._check_codec(codec, token_ids, sum(counts))
-        rows, offsets = self.rows(seqs, counts)
+        rows, offsets = self.rows(seqs, counts, positions)
         stream = self.torch.cuda.current_stream(self.device)
         return codec.encode(rows, token_ids, offsets, stream=stream), offsets

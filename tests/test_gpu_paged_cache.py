@@ -1,0 +1,67 @@
+"""PagedCache and the calls behind it on a GPU, against oracle/cache.py (fp64).  Tolerances as in
+test_gpu_cache.py; a row that was rotated on its way in and back on its way out has both passes'
+errors, the first one's turned (a pair's |a| + |b| grows by at most 2 in the turn)."""
+import numpy as np
+import pytest
+import torch
+
+import learned_kv_cache_dckv_b200 as D
+import oracle.cache as OC
+from test_gpu_cache import BF16, FP16, Paged, attend, check_attention, ints, normal, rope_tol, status, u, within
+
+pytestmark = pytest.mark.gpu
+
+
+def back_and_forth(x, dtype=BF16):
+    """Tolerance of keys x [n, heads, dim] rotated (half layout, whole head, magnitude 1) into
+    `dtype` and back: the forward pass rounds |y| <= |a| + |b| and errs by 8e-7 (|a| + |b|); the
+    inverse turns those errors of a pair into at most their sum, and adds its own, on inputs of
+    |y_a| + |y_b| <= 2 (|a| + |b|)."""
+    half = x.shape[-1] // 2
+    pair = (x[..., :half].double().abs() + x[..., half:].double().abs()).repeat(1, 1, 2)
+    first = 2 * pair * (u(dtype) + 8e-7)
+    return first + (x.double().abs() + first) * u(dtype) + 2 * pair * 8e-7
+
+
+# ------------------------------------------------------------------ rows of keys at positions of their own
+@pytest.mark.parametrize("dtype,layers,heads,dim,layout", [(BF16, 6, 2, 256, "half"), (FP16, 1, 3, 64, "interleaved")])
+def test_rows_at_given_positions(dtype, layers, heads, dim, layout):
+    lens, news = [40, 3, 20], [33, 0, 20]
+    c = Paged(201, lens, layers, heads, dim, 16, "token", dtype)
+    n, st = sum(news), status()
+    pos = torch.randint(0, 1 << 20, (n,), generator=torch.Generator().manual_seed(1)).int().cuda()
+    rows = torch.empty(n, layers * 2 * heads * dim, device="cuda", dtype=dtype)
+    D.dckv_cache_rows(c.pool, c.batch(news), rows, st, rope=D.rope_spec(dim, layout=layout, magnitude=1.5), positions=pos)
+    assert int(st) == 0
+    got, at = rows.view(n, layers, 2, heads, dim), 0
+    for b, new in enumerate(news):
+        pages, r = [t.cuda() for t in OC.slots(c.tables[b], new, 16)]
+        for l in range(layers if new else 0):
+            want, size = OC.rope(c.k[l, pages, r], pos[at: at + new], OC.rope_freq(dim), layout, "inverse", 1.5)
+            within(got[at: at + new, l, 0], want, rope_tol(want, size, dtype))
+            assert torch.equal(got[at: at + new, l, 1], c.v[l, pages, r])
+        at += new
+
+
+def test_paged_cache_gives_back_rows_at_their_positions():
+    """Tokens at their slots, then tokens at positions of their own: rows come back pre-RoPE when it
+    is told the positions, and not otherwise."""
+    cache = D.PagedCache(8, page_size=32)
+    a, b = cache.add(), cache.add()
+    k, v = normal(1, 6, 50, 2, 256), normal(2, 6, 50, 2, 256)
+    cache.append(cache.extend([a, b], [30, 20]), k, v)
+    k2, v2 = normal(3, 6, 7, 2, 256), normal(4, 6, 7, 2, 256)
+    own = ints(*range(1000, 7000, 1000), 5)
+    cache.append(cache.extend([a], [7]), k2, v2, positions=own)
+    with pytest.raises(D.DckvError):
+        cache.rows([a, b])
+    slots = lambda n: torch.arange(n, device="cuda", dtype=torch.int32)
+    for rows, offsets in (cache.rows([a, b], positions=torch.cat([slots(30), own, slots(20)])), cache.rows([a, b], [30, 20])):
+        r = rows.view(-1, 6, 2, 2, 256)
+        at = int(offsets[1])
+        for l in range(6):
+            want_k = torch.cat([k[l, :30], k2[l], k[l, 30:]]) if at == 37 else k[l]
+            want_v = torch.cat([v[l, :30], v2[l], v[l, 30:]]) if at == 37 else v[l]
+            within(r[:, l, 0], want_k.double(), back_and_forth(want_k))
+            assert torch.equal(r[:, l, 1], want_v)
+    assert int(cache.status) == 0

@@ -142,3 +142,58 @@ def test_store_counts_every_token_of_a_sequence(host):
     cache.store(codec, seqs, tokens(20), [20])
     cache.store(codec, seqs, tokens(21))
     cache.store(codec, seqs, None)  # a codec without mean models takes none
+
+
+# ------------------------------------------------------------------ keys that are not rotated at their slots
+def test_rows_refuses_keys_appended_with_positions_of_their_own(host):
+    cache, codec = host(), Codec()
+    a, b = seqs = cache.restore(codec, None, 0, tokens(30), offsets(20, 10))
+    cache.append(cache.extend([a], [3]), keys(cache, 3), keys(cache, 3), positions=tokens(3))
+    cache.append(cache.extend([b], [3]), keys(cache, 3), keys(cache, 3))
+    for call in (lambda: cache.rows(seqs), lambda: cache.rows([a], [21]), lambda: cache.store(codec, [a], tokens(23))):
+        with pytest.raises(D.DckvError) as e:
+            call()
+        assert e.value.code == D.DCKV_EINVAL
+    assert codec.calls == ["decode"]
+    cache.rows(seqs, [20, 13])  # the slots before them are as they were
+    where = torch.arange(36, dtype=torch.int32)
+    cache.rows(seqs, positions=where)  # told where, it passes that on
+    assert cache.calls[-1][0] == "dckv_cache_rows" and cache.calls[-1][2]["positions"] is where
+    cache.store(codec, seqs, tokens(36), positions=where)
+    assert cache.calls[-1][2]["positions"] is where and codec.calls[-1][1] == (36, 6144)
+
+
+def test_rows_refuses_keys_appended_as_they_come(host):
+    cache = host()
+    (a, b), batch = extended(cache, 5, 0)
+    cache.append(batch, keys(cache, 5), keys(cache, 5), rotate=False)
+    with pytest.raises(D.DckvError):
+        cache.rows([a])
+    cache.append(cache.extend([a, b], [2, 2]), keys(cache, 4), keys(cache, 4))
+    with pytest.raises(D.DckvError):
+        cache.rows([a, b])
+    cache.rows([b])
+    cache.drop(a)
+    c, batch = extended(cache, 4)
+    cache.append(batch, keys(cache, 4), keys(cache, 4))
+    cache.rows(c)
+
+
+def test_an_append_that_is_refused_marks_nothing(host, monkeypatch):
+    cache = host()
+    (a,), batch = extended(cache, 5)
+    with monkeypatch.context() as m:
+        m.setattr(D, "dckv_cache_append", lambda *_, **__: D._bad("refused"))
+        with pytest.raises(D.DckvError):
+            cache.append(batch, keys(cache, 5), keys(cache, 5), rotate=False)
+    cache.append(batch, keys(cache, 5), keys(cache, 5))
+    cache.rows([a])
+
+
+def test_a_batch_from_elsewhere_marks_every_sequence(host):
+    """cache_batch's own batches name pages, not sequences."""
+    cache = host()
+    (a,), batch = extended(cache, 5)
+    cache.append(D.cache_batch(*batch.tensors, 5), keys(cache, 5), keys(cache, 5), positions=tokens(5))
+    with pytest.raises(D.DckvError):
+        cache.rows([a])
