@@ -836,10 +836,12 @@ class PagedCache:
 
     def restore(self, codec, blob, blob_bytes, token_ids, seq_offsets):
         """Decodes a blob's prompts into new sequences of the pages (the decoder rotates the keys
-        as the codec's own rotation does).  The cache must have the codec's layers, heads, dims, type
-        and device.  Returns the sequences; codec.status has the decoder's status."""
+        as the codec's own rotation does).  The cache must have the codec's layers, heads, dims, type,
+        device and rotation.  Returns the sequences; codec.status has the decoder's status."""
         counts = [int(c) for c in np.diff(np.asarray(seq_offsets, np.int64))]
         self._check_codec(codec, token_ids, sum(counts))
+        if bytes(self.rope) != bytes(rope_spec(256)):
+            _bad("the cache's rotation is not the codec's (rope_spec(256)), which decoded keys come with")
         if min(counts) < 1:
             _bad("restore takes prompts of at least one token")
         stream = self.torch.cuda.current_stream(self.device)
@@ -872,8 +874,9 @@ class PagedCache:
 
     def store(self, codec, seqs, token_ids, counts=None, positions=None):
         """Encodes the sequences' first tokens with a codec: (blob, seq_offsets); codec.blob_size
-        and codec.status as after Codec.encode.  The cache must be one that restore takes; token_ids
-        has an id for each of those tokens (None for a codec that takes none); positions as for `rows`."""
+        and codec.status as after Codec.encode.  The cache must have the codec's layers, heads, dims,
+        type and device; token_ids has an id for each of those tokens (None for a codec that takes
+        none); positions as for `rows`."""
         counts = [self._len[s] for s in seqs] if counts is None else [int(c) for c in counts]
         self._check_codec(codec, token_ids, sum(counts))
         rows, offsets = self.rows(seqs, counts, positions)

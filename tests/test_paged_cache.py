@@ -197,3 +197,24 @@ def test_a_batch_from_elsewhere_marks_every_sequence(host):
     cache.append(D.cache_batch(*batch.tensors, 5), keys(cache, 5), keys(cache, 5), positions=tokens(5))
     with pytest.raises(D.DckvError):
         cache.rows([a])
+
+
+# ------------------------------------------------------------------ restore takes all or nothing
+@pytest.mark.parametrize("rope", [dict(rotary_dim=64), dict(rotary_dim=256, base=1e6),
+                                  dict(rotary_dim=256, layout="interleaved"), dict(rotary_dim=256, magnitude=1.5),
+                                  dict(rotary_dim=256, scaling="linear", factor=2.0)])
+def test_restore_refuses_a_cache_with_another_rotation(host, rope):
+    """The decoder rotates by the codec's own rotation; the cache would append, attend and rotate
+    back by another."""
+    cache, codec = host(rope=D.rope_spec(**rope)), Codec()
+    with pytest.raises(D.DckvError) as e:
+        cache.restore(codec, None, 0, tokens(20), offsets(20))
+    assert e.value.code == D.DCKV_EINVAL and codec.calls == [] and cache._len == {}
+
+
+def test_restore_takes_the_codecs_rotation_however_it_was_made(host):
+    spec = D.rope_spec(256)
+    same = D.RopeSpec(256, 0, 1.0, (ctypes.c_double * 128)(*spec.freq))
+    for rope in (None, spec, same):
+        cache = host(rope=rope)
+        assert [cache.length(s) for s in cache.restore(Codec(), None, 0, tokens(20), offsets(20))] == [20]
