@@ -848,12 +848,11 @@ class PagedCache:
         k, v = codec.decode(blob, blob_bytes, token_ids, seq_offsets, stream=stream)
         seqs = [self.add() for _ in counts]
         try:
-            batch = self.extend(seqs, counts)
-        except DckvError:
+            dckv_cache_append(self.pool, self.extend(seqs, counts), k, v, self.status)
+        except BaseException:
             for s in seqs:
                 self.drop(s)
             raise
-        dckv_cache_append(self.pool, batch, k, v, self.status)
         return seqs
 
     def rows(self, seqs, counts=None, positions=None):

@@ -218,3 +218,26 @@ def test_restore_takes_the_codecs_rotation_however_it_was_made(host):
     for rope in (None, spec, same):
         cache = host(rope=rope)
         assert [cache.length(s) for s in cache.restore(Codec(), None, 0, tokens(20), offsets(20))] == [20]
+
+
+@pytest.mark.parametrize("error", [D.DckvError(D.DCKV_ECUDA, "launch"), RuntimeError("out of memory")])
+@pytest.mark.parametrize("where", ["dckv_cache_append", "cache_batch"])
+def test_restore_gives_its_pages_back_when_a_call_fails(host, monkeypatch, where, error):
+    cache = host()
+
+    def fail(*a, **kw):
+        raise error
+
+    with monkeypatch.context() as m:
+        m.setattr(D, where, fail)
+        with pytest.raises(type(error)):
+            cache.restore(Codec(), None, 0, tokens(53), offsets(20, 33))
+    assert cache._len == {} and cache._pages == {} and sorted(cache._free) == list(range(8))
+    assert [cache.length(s) for s in cache.restore(Codec(), None, 0, tokens(53), offsets(20, 33))] == [20, 33]
+
+
+def test_restore_without_room_takes_nothing(host):
+    cache, codec = host(n_pages=4), Codec()
+    with pytest.raises(D.DckvError) as e:
+        cache.restore(codec, None, 0, tokens(53), offsets(20, 33))
+    assert e.value.code == D.DCKV_ECAPACITY and cache._len == {} and sorted(cache._free) == list(range(4))
