@@ -799,7 +799,13 @@ class PagedCache:
         for s, c, m in zip(seqs, counts, need):
             self._pages[s] += [self._free.pop() for _ in range(m)]
             self._len[s] += c
-        return self._batch(seqs, counts)
+        try:
+            return self._batch(seqs, counts)
+        except BaseException:
+            for s, c, m in reversed(list(zip(seqs, counts, need))):
+                self._free += [self._pages[s].pop() for _ in range(m)]
+                self._len[s] -= c
+            raise
 
     def append(self, batch, k, v, q=None, q_out=None, rotate=True, positions=None):
         """dckv_cache_append with the cache's rotation (rotate=False: keys come rotated).  Keys that it

@@ -241,3 +241,19 @@ def test_restore_without_room_takes_nothing(host):
     with pytest.raises(D.DckvError) as e:
         cache.restore(codec, None, 0, tokens(53), offsets(20, 33))
     assert e.value.code == D.DCKV_ECAPACITY and cache._len == {} and sorted(cache._free) == list(range(4))
+
+
+def test_extend_takes_nothing_when_its_batch_fails(host, monkeypatch):
+    cache = host()
+    a, b = cache.add(), cache.add()
+    cache.extend([a], [20])
+    before = {s: list(p) for s, p in cache._pages.items()}, dict(cache._len), list(cache._free)
+
+    def fail(*args):
+        raise RuntimeError("out of memory")
+
+    with monkeypatch.context() as m:
+        m.setattr(D, "cache_batch", fail)
+        with pytest.raises(RuntimeError):
+            cache.extend([a, b], [20, 17])
+    assert (cache._pages, cache._len, cache._free) == before
