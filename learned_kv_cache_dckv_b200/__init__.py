@@ -848,7 +848,7 @@ class PagedCache:
         self._check_codec(codec, token_ids, sum(counts))
         if bytes(self.rope) != bytes(rope_spec(256)):
             _bad("the cache's rotation is not the codec's (rope_spec(256)), which decoded keys come with")
-        if min(counts) < 1:
+        if not counts or min(counts) < 1:
             _bad("restore takes prompts of at least one token")
         stream = self.torch.cuda.current_stream(self.device)
         k, v = codec.decode(blob, blob_bytes, token_ids, seq_offsets, stream=stream)
@@ -861,12 +861,19 @@ class PagedCache:
             raise
         return seqs
 
+    def _counts(self, seqs, counts):
+        lens = [self._len[s] for s in seqs]
+        counts = lens if counts is None else [int(c) for c in counts]
+        if not lens or len(counts) != len(lens) or any(not 0 <= c <= n for c, n in zip(counts, lens)):
+            _bad(f"counts {counts} are not within the sequences' lengths {lens}")
+        return counts
+
     def rows(self, seqs, counts=None, positions=None):
         """The first counts[i] (default: all) tokens of each sequence as pre-RoPE rows, and their
         offsets: the arguments of Codec.encode.  Keys are rotated back from their slots or, if given,
         from positions (device int32, one per row); a key that `append` did not rotate at its slot
         needs them."""
-        counts = [self._len[s] for s in seqs] if counts is None else [int(c) for c in counts]
+        counts = self._counts(seqs, counts)
         for s, c in zip(seqs, counts):
             if positions is None and c > self._odd.get(s, c):
                 _bad(f"keys of sequence {s} are not rotated at their slots from slot {self._odd[s]} on: "
@@ -882,7 +889,7 @@ class PagedCache:
         and codec.status as after Codec.encode.  The cache must have the codec's layers, heads, dims,
         type and device; token_ids has an id for each of those tokens (None for a codec that takes
         none); positions as for `rows`."""
-        counts = [self._len[s] for s in seqs] if counts is None else [int(c) for c in counts]
+        counts = self._counts(seqs, counts)
         self._check_codec(codec, token_ids, sum(counts))
         rows, offsets = self.rows(seqs, counts, positions)
         stream = self.torch.cuda.current_stream(self.device)

@@ -257,3 +257,33 @@ def test_extend_takes_nothing_when_its_batch_fails(host, monkeypatch):
         with pytest.raises(RuntimeError):
             cache.extend([a, b], [20, 17])
     assert (cache._pages, cache._len, cache._free) == before
+
+
+# ------------------------------------------------------------------ counts that the host can check
+@pytest.mark.parametrize("counts", [[21, 5], [20, -1], [20], [20, 5, 1]])
+def test_rows_and_store_refuse_counts_that_the_sequences_do_not_have(host, counts):
+    """Rows past a sequence's length would be left as the allocation had them."""
+    cache, codec = host(), Codec()
+    seqs, _ = extended(cache, 20, 5)
+    for call in (lambda: cache.rows(seqs, counts), lambda: cache.store(codec, seqs, tokens(64), counts)):
+        with pytest.raises(D.DckvError) as e:
+            call()
+        assert e.value.code == D.DCKV_EINVAL
+    assert codec.calls == [] and cache.calls == []
+
+
+def test_rows_store_and_restore_refuse_no_sequences(host):
+    cache, codec = host(), Codec()
+    for call in (lambda: cache.rows([]), lambda: cache.store(codec, [], tokens(0)),
+                 lambda: cache.restore(codec, None, 0, tokens(0), offsets())):
+        with pytest.raises(D.DckvError):
+            call()
+    assert codec.calls == []
+
+
+def test_rows_takes_parts_of_sequences(host):
+    cache = host()
+    seqs, _ = extended(cache, 20, 5, 0)
+    for counts, want in ((None, [0, 20, 25, 25]), ([0, 5, 0], [0, 0, 5, 5]), ([20, 1, 0], [0, 20, 21, 21])):
+        rows, offs = cache.rows(seqs, counts)
+        assert offs.tolist() == want and rows.shape == (want[-1], 6144)
