@@ -497,15 +497,17 @@ def kv_pool(k, v) -> KvPool:
     L, pages, rows, heads, dim = k.shape
     p = KvPool(k.data_ptr(), v.data_ptr(), dev, code, L, heads, dim, rows, pages, *ks[:4], *vs[:4])
     p.tensors = (k, v)
-    # what the calls below compare with (a ctypes field is slower to read)
-    p.dev, p.dt, p.kv_shape, p.dim, p.ref = dev, k.dtype, (L, heads, dim), dim, ctypes.byref(p)
+    # what the calls below compare with and pass on (a ctypes field is slower to read; a byref kept here
+    # would hold p, which holds it: the tensors would live until a collection of cycles)
+    p.dev, p.dt, p.kv_shape, p.dim, p.ref = dev, k.dtype, (L, heads, dim), dim, ctypes.addressof(p)
     return p
 
 
 def cache_batch(offsets, kv_lens, page_table, max_new) -> CacheBatch:
     """Describes the sequences of a call: int32 offsets [batch + 1], kv_lens [batch] and
     page_table [batch, pages] on the pool's device; max_new bounds any sequence's new tokens.
-    Keeps the tensors alive; their contents may change between calls (and graph replays)."""
+    Keeps the tensors alive; their contents may change between calls (and graph replays: keep the
+    batch as long as a graph that was captured with it)."""
     if kv_lens.dim() != 1 or offsets.shape != (kv_lens.shape[0] + 1,) or page_table.dim() != 2 or \
             page_table.shape[0] != kv_lens.shape[0]:
         _bad("offsets, kv_lens and page_table must be [batch + 1], [batch] and [batch, pages]")
@@ -516,7 +518,7 @@ def cache_batch(offsets, kv_lens, page_table, max_new) -> CacheBatch:
     b = CacheBatch(kv_lens.shape[0], int(max_new), page_table.shape[1], 0, _int32_on(dev, "offsets", offsets),
                    _int32_on(dev, "kv_lens", kv_lens), page_table.data_ptr(), st[0])
     b.tensors = (offsets, kv_lens, page_table)
-    b.dev, b.ref = dev, ctypes.byref(b)
+    b.dev, b.ref = dev, ctypes.addressof(b)
     return b
 
 

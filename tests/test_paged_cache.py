@@ -287,3 +287,21 @@ def test_rows_takes_parts_of_sequences(host):
     for counts, want in ((None, [0, 20, 25, 25]), ([0, 5, 0], [0, 0, 5, 5]), ([20, 1, 0], [0, 20, 21, 21])):
         rows, offs = cache.rows(seqs, counts)
         assert offs.tolist() == want and rows.shape == (want[-1], 6144)
+
+
+# ------------------------------------------------------------------ lifetimes
+def test_descriptors_do_not_outlive_their_last_reference(host):
+    """A pool's pages and a batch's arrays go with it, not with a later collection of cycles."""
+    cache = host()
+    seqs, batch = extended(cache, 5)
+    gone = [weakref.ref(t) for t in (cache.k, cache.v, *batch.tensors)]
+    assert all(r() is not None for r in gone)
+    gc.collect()
+    gc.disable()
+    try:
+        del batch
+        assert all(r() is None for r in gone[2:])
+        del cache
+        assert all(r() is None for r in gone)
+    finally:
+        gc.enable()
