@@ -756,7 +756,7 @@ class PagedCache:
         self._free = list(range(n_pages - 1, -1, -1))
         self._pages, self._len = {}, {}
         self._odd = {}  # sequences with keys that are not rotated at their slots: the first such slot
-        self._ws = None
+        self._ws = []  # growing sizes, none given back: a captured graph may write any of them
         self._next = 0
 
     def add(self) -> int:
@@ -822,14 +822,16 @@ class PagedCache:
                     self._odd[s] = min(first, self._odd.get(s, first))
 
     def attend(self, layer, batch, q, out=None, scale=None, causal=True, lse=None):
-        """dckv_attention on the cache's workspace; out is a new tensor unless given."""
+        """dckv_attention on the cache's workspace; out is a new tensor unless given.  Keep the cache as
+        long as a graph that was captured with it."""
         need = dckv_attention_workspace_bytes(self.pool, batch, q.shape[1])
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
+        ws = next((w for w in self._ws if w.numel() >= need), None)
+        if ws is None:
+            ws = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
+            self._ws.append(ws)
         if out is None:
             out = self.torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        return dckv_attention(self.pool, layer, batch, q, out, self.status, self._ws, scale=scale, causal=causal,
-                              lse=lse)
+        return dckv_attention(self.pool, layer, batch, q, out, self.status, ws, scale=scale, causal=causal, lse=lse)
 
     def _check_codec(self, codec, token_ids, n_tokens):
         """The codec's calls take rows of its own shape and type, and the tokens' ids, on trust."""

@@ -305,3 +305,22 @@ def test_descriptors_do_not_outlive_their_last_reference(host):
         assert all(r() is None for r in gone)
     finally:
         gc.enable()
+
+
+def test_a_larger_call_leaves_the_workspace_of_captured_ones(host, monkeypatch):
+    """A captured graph writes the workspace of its capture on every replay, so that memory must stay
+    the cache's when another call needs more."""
+    cache = host()
+    (a,), batch = extended(cache, 5)
+    q = torch.zeros(5, 8, 256, dtype=torch.bfloat16)
+    used = []
+    monkeypatch.setattr(D, "dckv_attention", lambda *args, **kw: used.append(args[6]))
+    for need in (1000, 5000, 1000, 9000, 5000):
+        monkeypatch.setattr(D, "dckv_attention_workspace_bytes", lambda *args, n=need: n)
+        cache.attend(0, batch, q)
+        assert used[-1].numel() >= need
+    at = [t.data_ptr() for t in used]
+    alive = {i: weakref.ref(t) for i, t in enumerate(used)}
+    used.clear()
+    gc.collect()
+    assert all(r() is not None and r().data_ptr() == at[i] for i, r in alive.items())
