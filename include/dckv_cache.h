@@ -164,7 +164,8 @@ int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch *batch, con
 /* out[t][h] = sum_j softmax_j(scale q[t][h] . k[j][h / g]) v[j][h / g] over the slots j that
  * token t of sequence b sees: all j < kv_lens[b], or with `causal` those with
  * j <= kv_lens[b] - n_b + t (the new tokens are the sequence's last, already appended);
- * g = n_q_heads / n_kv_heads.  A token that sees no slot gets out = 0 and lse = -infinity.
+ * g = n_q_heads / n_kv_heads.  A token that sees no slot gets out = 0 and lse = -infinity;
+ * one that sees slots and whose query holds NaN gets NaN in both.
  * lse (natural logarithm of sum_j exp(scale q . k)) allows outputs over disjoint sets of slots
  * to be joined.  Slots that a sequence does not use may hold anything; keys and values that
  * are in use must be finite (a value beyond the causal bound of one row may still be

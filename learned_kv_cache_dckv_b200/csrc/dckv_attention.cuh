@@ -357,6 +357,12 @@ __device__ __forceinline__ bool attn_plan(const BatchDev &bt, const AttnDev &a, 
   return true;
 }
 
+// A row's lse from its reference (log2 units) and its sum: -infinity where it saw no slot, NaN where its
+// scores held one.
+__device__ __forceinline__ float row_lse(float ref, float sum) {
+  return sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+}
+
 // ------------------------------------------------------------------ math helpers
 __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp and flush to zero (PTX ex2.approx.ftz)
   float y;
@@ -758,7 +764,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
         store4<T>(reinterpret_cast<T *>(a.out) + tok * a.ot + head * a.oh + d,
                   make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         if (a.lse && d == 0)
-          a.lse[tok * a.heads + head] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          a.lse[tok * a.heads + head] = row_lse(top, sum);
       } else {
         a.part_o[((int64_t)slot * C::ROWS + r) * (D / 4) + d / 4] = acc;
         if (d == 0) a.part_ml[slot * C::ROWS + r] = make_float2(top, sum);
@@ -1198,7 +1204,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
         if (valid && half == 0 && ok) {
           if (!(begins && ends)) a.part_ml[(int64_t)slot * PAIR_ROWS + prow] = make_float2(ref, sum);
-          else if (a.lse) a.lse[tok * a.heads + head] = sum > 0.f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          else if (a.lse) a.lse[tok * a.heads + head] = row_lse(ref, sum);
         }
       }
       if (begins && !ends && rank == 0 && sw == 0 && lane == 0) describe(a, pl, w, c, sh.rows);
@@ -1297,7 +1303,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_few(const AttnDev a, int 
         *reinterpret_cast<Vec<T, V> *>(out + (v * 32 + lane) * V) = y;
       }
       if (a.lse && lane == 0)
-        a.lse[tok * a.heads + head] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        a.lse[tok * a.heads + head] = row_lse(m, sum);
     }
     if (shared_row) __syncthreads();
   }
@@ -1361,7 +1367,7 @@ __device__ __forceinline__ void join_store(const JoinAcc &acc, const AttnDev &a,
   for (int k = 0; k < JOIN_STEPS; ++k)
     store4<T>(out + k * 16, make_float4(acc.o[k].x * inv, acc.o[k].y * inv, acc.o[k].z * inv, acc.o[k].w * inv));
   if (a.lse && q == 0 && k0 == 0)
-    a.lse[tok * a.heads + head] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * 0.6931471805599453f : -INFINITY;
+    a.lse[tok * a.heads + head] = row_lse(acc.m, acc.l);
 }
 
 template <typename T, int D>
