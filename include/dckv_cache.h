@@ -170,8 +170,9 @@ int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch *batch, con
  * to be joined.  Slots that a sequence does not use may hold anything; keys and values that
  * are in use must be finite (a value beyond the causal bound of one row may still be
  * multiplied by that row's weight 0).
- * Scores, maxima, sums and outputs are fp32; the weights are rounded to the cache's type
- * (relative to the row's running maximum) before they multiply v, and out is rounded once.
+ * Scores, maxima, sums and outputs are fp32; the weights are rounded to the cache's type before
+ * they multiply v (by at most half a step of each weight; in fp16 a weight below 2^-21 of the row's
+ * largest by at most 2^-32 of that one), and out is rounded once.
  * For a given device and arguments, the result is the same on every call; a sequence's bits
  * may depend on the other sequences of the call, which decide where its slots are split. */
 typedef struct {

@@ -392,6 +392,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Weights are rounded to the cache's type before they multiply V (the tensor cores take no more), each
+// relative to itself as long as it is a normal number there.  bf16 has fp32's range, but fp16 ends at
+// 2^-14: of weights relative to a row's largest, those below 2^-25 would vanish and those above lose
+// bits, and thousands of slots of them count beside one large score.  So in fp16 the reference lies
+// below the largest score, and the weights reach up to 2^15, just under its largest number: 2^-25 is
+// then 2^-40 of the largest weight for few rows, and 2^-32 or less for the pairs, whose largest may
+// first grow by RESCALE_STEPS.
+template <typename T>
+constexpr float weight_head(float slack) {  // log2 of the largest weight when the reference is set
+  return std::is_same<T, __half>::value ? 15.f - slack : 0.f;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          top = fmaxf(top, m[2 * nt + e]);
+          top = fmaxf(top - weight_head<T>(0.f), m[2 * nt + e]);
           const float ref = top == -INFINITY ? 0.f : top;
           keep[e] = exp2_fast(m[2 * nt + e] - ref);
           m[2 * nt + e] = top;
@@ -796,8 +808,8 @@ __global__ void __launch_bounds__(DEC_ATTN_THREADS, 1)
 // row, 64 columns each, which exchange the row maximum through shared memory.  While they work
 // on tile j the tensor cores run S(j + 1), then O(j).
 // The maximum a row's weights refer to moves only when the true one exceeds it by more than
-// RESCALE_STEPS in log2: until then P stays below 2^RESCALE_STEPS, exactly representable ranges
-// in both types, and O needs no rescaling, which costs a round trip of O through registers.
+// RESCALE_STEPS in log2: until then P stays below 2^RESCALE_STEPS (2^15 in fp16, see weight_head) and
+// O needs no rescaling, which costs a round trip of O through registers.
 constexpr int PAIR_ROWS = 256;
 constexpr int PAIR_KEYS = 128;
 constexpr int PAIR_SOFT_WARPS = 8;
@@ -850,6 +862,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   using C = PairAttn<D>;
   constexpr int STAGES = C::STAGES;
   constexpr uint32_t S_COL = 256;
+  constexpr float HEAD = weight_head<T>(RESCALE_STEPS);
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   // no room for slack: the swizzled tiles rely on dynamic shared memory starting on 1,024 bytes
   // (it does where a kernel has no static shared memory)
@@ -1118,9 +1131,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           xc[half * 128 + row] = mine;
           named_bar_sync(1 + quarter, 64);
           const float top = fmaxf(mine, xc[(half ^ 1) * 128 + row]);
-          const bool move = top > ref + RESCALE_STEPS;
+          const bool move = top > ref + (HEAD + RESCALE_STEPS);
           if (__any_sync(0xffffffffu, move)) {
-            const float next = move ? top : ref;
+            const float next = move ? top - HEAD : ref;
             const float f = move ? exp2_fast(ref - next) : 1.f;
             sum *= f;
             ref = next;

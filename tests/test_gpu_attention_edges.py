@@ -1,8 +1,11 @@
-"""Attention over the pages where its kernels treat rows apart: queries that hold NaN."""
+"""Attention over the pages where its kernels treat rows apart: queries that hold NaN, and fp16
+weights far below a row's largest.  Against oracle/cache.py (fp64); tolerances as in
+test_gpu_cache.py."""
 import pytest
 import torch
 
-from test_gpu_cache import Paged, attend, normal
+import oracle.cache as OC
+from test_gpu_cache import EXP_ERR, FP16, Paged, attend, normal, u, within
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +37,30 @@ def test_attention_nan_that_sees_nothing(dim, new):
     _, out, lse = attend(c, [new], 2, q=q)
     assert bool((out[:-1] == 0).all()) and bool((lse[:-1] == -float("inf")).all())
     assert bool(out[-1].isfinite().all()) and bool(lse[-1].isfinite().all())
+
+
+# ------------------------------------------------------------------ fp16 weights below its normal range
+@pytest.mark.parametrize("dim,group", [(64, 2), (128, 12), (256, 8), (64, 20), (128, 20), (256, 20)])
+def test_attention_fp16_small_weights(dim, group):
+    """One key of each sequence scores 17 above all others (weights of e^-17 = 2^-24.5), and only the
+    others' values are not 0.  A weight w of the row's largest is held as fp16(w 2^h) with h >= 7: off
+    by u(fp16) relative where that is a normal number, by 2^-25 - h <= 2^-32 absolute below; the second
+    adds sum |v| 2^-32 at most.  (In a step of 2^-24 each of these weights would be off by 44%.)"""
+    count, length = 150, 1200
+    c = Paged(305, [length] * count, 1, 1, dim, 16, dtype=FP16)
+    c.k[:] = 0
+    c.v.uniform_(2.0, 6.0)
+    first = torch.tensor([t[0] for t in c.tables], device="cuda")
+    c.k[0, first, 0, 0, 0] = 17.0
+    c.v[0, first, 0] = 0.0
+    q = torch.zeros(count, group, dim, device="cuda", dtype=FP16)
+    q[..., 0] = 1.0
+    news = [1] * count
+    _, out, lse = attend(c, news, group, q=q, scale=1.0)
+    some = 8  # sequences that the definition is worked out for; they are alike but for their values
+    want, want_lse, mass, reach = OC.attention(q[:some], c.k[0], c.v[0], news[:some], c.lens[:some], c.tables[:some], 1.0,
+                                               True)
+    ds = reach * (dim + 8) * 2.0 ** -23
+    rel = (u(FP16) + 2.2 * ds + (length + 64) * 2.0 ** -23 + EXP_ERR)[..., None]
+    within(out[:some], want, want.abs() * u(FP16) + mass * rel + length * 6.0 * 2.0 ** -32, "out")
+    within(lse[:some], want_lse, ds + EXP_ERR + (length + 64) * 2.0 ** -23 + want_lse.abs() * 2.0 ** -22, "lse")
