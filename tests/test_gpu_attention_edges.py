@@ -1,11 +1,11 @@
-"""Attention over the pages where its kernels treat rows apart: queries that hold NaN, and fp16
-weights far below a row's largest.  Against oracle/cache.py (fp64); tolerances as in
-test_gpu_cache.py."""
+"""Attention over the pages where its kernels treat rows apart: queries that hold NaN, fp16 weights
+far below a row's largest, and pages that a whole key tile fits in.  Against oracle/cache.py (fp64);
+tolerances as in test_gpu_cache.py."""
 import pytest
 import torch
 
 import oracle.cache as OC
-from test_gpu_cache import EXP_ERR, FP16, Paged, attend, normal, u, within
+from test_gpu_cache import BF16, EXP_ERR, FP16, Paged, attend, check_attention, normal, u, within
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,26 @@ def test_attention_fp16_small_weights(dim, group):
     rel = (u(FP16) + 2.2 * ds + (length + 64) * 2.0 ** -23 + EXP_ERR)[..., None]
     within(out[:some], want, want.abs() * u(FP16) + mass * rel + length * 6.0 * 2.0 ** -32, "out")
     within(lse[:some], want_lse, ds + EXP_ERR + (length + 64) * 2.0 ** -23 + want_lse.abs() * 2.0 ** -22, "lse")
+
+
+# ------------------------------------------------------------------ pages of a key tile and more
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype,order,page", [(BF16, "token", 128), (FP16, "head", 128), (BF16, "head", 256),
+                                              (FP16, "token", 384)])
+@pytest.mark.parametrize("group,causal", [(3, True), (8, False)])
+def test_attention_large_pages(dim, dtype, order, page, group, causal):
+    """Lengths of 1, 127, 128, 129 and 255 beyond whole pages: one box holds a tile's values, and up to
+    127 of its rows behind the last slot hold NaN."""
+    lens = [1, 127, 128, 129, 255, page + 1, page + 127, 2 * page + 128, 2 * page + 129, page + 255]
+    news = [1, 127, 40, 129, 0, 33, 1, 64, 9, 100]
+    c = Paged(307, lens, 1, 2, dim, page, order, dtype)
+    check_attention(c, news, 2 * group, causal, pad=1)
+    check_attention(c, [1] * len(lens), 2 * group, causal)  # single tokens
+
+
+@pytest.mark.parametrize("dim,group", [(64, 5), (128, 3), (256, 4)])
+@pytest.mark.parametrize("page", [128, 256])
+def test_attention_large_pages_many_tiles_per_block(dim, group, page):
+    lens, news = [1577, 1416, 926, 2099, 1820, 700, 1501], [77, 33, 43, 31, 21, 129 // group, 0]
+    c = Paged(309, lens, 1, 4, dim, page)
+    check_attention(c, news, 4 * group)
