@@ -737,10 +737,11 @@ class PagedCache:
     sequence's pages and length (on the host), and makes the calls of dckv_cache.h on them.
 
     A step: ``batch = cache.extend(seqs, counts)`` gives the sequences room for their new tokens;
-    then per layer or at once ``cache.append(batch, k, v, q=q)`` and
-    ``cache.attend(layer, batch, q)``.  ``restore`` and ``store`` move whole prompts between
-    blobs of a Codec and the pages.  Everything runs on the current stream of the cache's device;
-    calls on one cache that overlap in time (two streams) need ordering between them."""
+    then, layer by layer, ``cache.append(batch, k, v, q=q, q_out=q_rot, layer=layer)`` and
+    ``cache.attend(layer, batch, q_rot)`` (without `layer`, append takes all layers' at once).
+    ``restore`` and ``store`` move whole prompts between blobs of a Codec and the pages.  Everything
+    runs on the current stream of the cache's device; calls on one cache that overlap in time (two
+    streams) need ordering between them."""
 
     def __init__(self, n_pages, page_size=64, n_layers=6, n_kv_heads=2, head_dim=256, dtype=None, device=0, rope=None):
         import torch
@@ -751,6 +752,7 @@ class PagedCache:
         self.k = torch.empty(shape, dtype=dtype or torch.bfloat16, device=self.device)
         self.v = torch.empty_like(self.k)
         self.pool = kv_pool(self.k, self.v)
+        self._layers = [kv_pool(self.k[l], self.v[l]) for l in range(n_layers)]
         self.rope = rope_spec(head_dim) if rope is None else rope
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._free = list(range(n_pages - 1, -1, -1))
@@ -809,12 +811,15 @@ class PagedCache:
                 self._len[s] -= c
             raise
 
-    def append(self, batch, k, v, q=None, q_out=None, rotate=True, positions=None):
-        """dckv_cache_append with the cache's rotation (rotate=False: keys come rotated).  Keys that it
+    def append(self, batch, k, v, q=None, q_out=None, rotate=True, positions=None, layer=None):
+        """dckv_cache_append with the cache's rotation (rotate=False: keys come rotated): k and v of all
+        layers [layers, n, heads, dim] or, with `layer`, of that one [n, heads, dim].  Keys that it
         did not rotate at their slots (rotate=False, or positions given) come back by `rows` and
         `store` only where these are given positions; a replayed graph is judged by its capture."""
-        dckv_cache_append(self.pool, batch, k, v, self.status, rope=self.rope if rotate else None, positions=positions,
-                          q=q, q_out=q_out)
+        if layer is not None and not 0 <= layer < self.pool.n_layers:
+            _bad(f"layer {layer} out of range")
+        dckv_cache_append(self.pool if layer is None else self._layers[layer], batch, k, v, self.status,
+                          rope=self.rope if rotate else None, positions=positions, q=q, q_out=q_out)
         if not rotate or positions is not None:
             # a batch that extend did not make does not say whose slots it writes
             for s, first in getattr(batch, "firsts", dict.fromkeys(self._len, 0)).items():

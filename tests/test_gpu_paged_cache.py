@@ -65,3 +65,37 @@ def test_paged_cache_gives_back_rows_at_their_positions():
             within(r[:, l, 0], want_k.double(), back_and_forth(want_k))
             assert torch.equal(r[:, l, 1], want_v)
     assert int(cache.status) == 0
+
+
+# ------------------------------------------------------------------ a model's step
+@pytest.mark.parametrize("dtype,heads,dim", [(BF16, 2, 256), (FP16, 1, 64)])
+def test_append_layer_by_layer(dtype, heads, dim):
+    """Layer l + 1's keys come out of layer l's attention: append and attend in turn.  The pages and
+    outputs are those of keys appended at once."""
+    L, group = 4, 4
+    caches = [D.PagedCache(12, 32, L, heads, dim, dtype) for _ in range(2)]
+    seqs = [[c.add(), c.add()] for c in caches]
+    mix = normal(1, L, heads * group * dim, (group + 2) * heads * dim, dtype=dtype, gain=(heads * group * dim) ** -0.5)
+    x = normal(2, 45, heads * group * dim, dtype=dtype)
+    at = 0
+    for counts in ([40, 3], [1, 1]):
+        n = sum(counts)
+        batches = [c.extend(s, counts) for c, s in zip(caches, seqs)]
+        h, kept = x[at: at + n], []
+        for l in range(L):
+            q, k, v = (h @ mix[l]).view(n, -1, dim).split([group * heads, heads, heads], 1)
+            turned = torch.empty_like(q.contiguous())
+            caches[0].append(batches[0], k, v, q=q, q_out=turned, layer=l)
+            out = caches[0].attend(l, batches[0], turned)
+            kept.append((k, v, turned, out))
+            h = out.flatten(1)
+        caches[1].append(batches[1], *[torch.stack([s[i] for s in kept]) for i in (0, 1)])
+        for l, (_, _, turned, out) in enumerate(kept):
+            assert torch.equal(caches[1].attend(l, batches[1], turned), out)
+        at += n
+    for a, b in zip(*seqs):
+        pages, rows = [t.cuda() for t in OC.slots(caches[0]._pages[a], caches[0].length(a), 32)]
+        assert caches[0]._pages[a] == caches[1]._pages[b]
+        assert torch.equal(caches[0].k[:, pages, rows], caches[1].k[:, pages, rows])
+        assert torch.equal(caches[0].v[:, pages, rows], caches[1].v[:, pages, rows])
+    assert int(caches[0].status) == 0 and int(caches[1].status) == 0

@@ -324,3 +324,27 @@ def test_a_larger_call_leaves_the_workspace_of_captured_ones(host, monkeypatch):
     used.clear()
     gc.collect()
     assert all(r() is not None and r().data_ptr() == at[i] for i, r in alive.items())
+
+
+# ------------------------------------------------------------------ layer by layer
+def test_append_takes_one_layer(host):
+    cache = host(n_layers=3)
+    _, batch = extended(cache, 5)
+    k = torch.zeros(5, 2, 256, dtype=torch.bfloat16)
+    for layer in (0, 2):
+        cache.append(batch, k, k, layer=layer)
+        pool = cache.calls[-1][1][0]
+        assert pool.kv_shape == (1, 2, 256) and pool.n_pages == 8
+        assert pool.k == cache.k[layer].data_ptr() and pool.v == cache.v[layer].data_ptr()
+    cache.append(batch, keys(cache, 5), keys(cache, 5))
+    assert cache.calls[-1][1][0] is cache.pool
+
+
+@pytest.mark.parametrize("layer", [-1, 3])
+def test_append_refuses_a_layer_that_is_not_there(host, layer):
+    cache = host(n_layers=3)
+    _, batch = extended(cache, 5)
+    k = torch.zeros(5, 2, 256, dtype=torch.bfloat16)
+    with pytest.raises(D.DckvError) as e:
+        cache.append(batch, k, k, layer=layer)
+    assert e.value.code == D.DCKV_EINVAL and cache.calls == []
