@@ -64,7 +64,7 @@ extern "C" {
 typedef struct {
   int32_t rotary_dim; /* even, 2 .. 2 * DCKV_ROPE_MAX_PAIRS                                */
   int32_t layout;     /* DCKV_ROPE_HALF or DCKV_ROPE_INTERLEAVED                           */
-  double magnitude;   /* finite, > 0                                                       */
+  double magnitude;   /* 2^-126 .. 2^126                                                   */
   double freq[DCKV_ROPE_MAX_PAIRS]; /* the first rotary_dim / 2 are used                   */
 } dckv_rope_spec;
 

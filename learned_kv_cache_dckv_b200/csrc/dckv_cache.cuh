@@ -373,8 +373,8 @@ static int check_spec(const dckv_rope_spec *s, int mode, RopeDev &d) {
     return fail(DCKV_EINVAL, "unknown rotary layout %d", s->layout);
   if (mode != DCKV_ROPE_FORWARD && mode != DCKV_ROPE_GRADIENT && mode != DCKV_ROPE_INVERSE)
     return fail(DCKV_EINVAL, "unknown rotary mode %d", mode);
-  if (!std::isfinite(s->magnitude) || !(s->magnitude > 0.0))
-    return fail(DCKV_EINVAL, "rotary magnitude must be finite and positive");
+  if (!(s->magnitude >= 0x1p-126) || !(s->magnitude <= 0x1p126))  // it and its inverse are normal fp32 numbers
+    return fail(DCKV_EINVAL, "rotary magnitude must be within 2^-126 .. 2^126");
   for (int i = 0; i < s->rotary_dim / 2; ++i) {
     if (!std::isfinite(s->freq[i])) return fail(DCKV_EINVAL, "rotary frequency %d is not finite", i);
     d.turns[i] = s->freq[i] * 0.15915494309189535;  // 1 / (2 pi)

@@ -191,3 +191,19 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(D.DckvError):
         D.cache_batch(torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                       torch.zeros(2, 4, dtype=torch.int32), 1)
+
+
+@pytest.mark.parametrize("magnitude", [1e39, 1e-39, 1e300, 1e-300, 2.0 ** 127, 2.0 ** -127])
+def test_rope_magnitude_that_fp32_does_not_hold(magnitude):
+    """The kernels multiply by m and 1 / m in fp32: infinity would make NaN of a 0, and 0 everything 0."""
+    with pytest.raises(D.DckvError) as e:
+        D.rope_spec(64, magnitude=magnitude)
+    assert e.value.code == D.DCKV_EINVAL
+    spec = D.rope_spec(64)
+    spec.magnitude = magnitude
+    assert all(_rope(spec=spec, mode=m) == D.DCKV_EINVAL for m in D.ROPE_MODES.values())
+
+
+@pytest.mark.parametrize("magnitude", [2.0 ** 126, 2.0 ** -126, 1.0, 0.8])
+def test_rope_magnitude_that_fp32_holds(magnitude):
+    assert D.rope_spec(64, magnitude=magnitude).magnitude == magnitude
