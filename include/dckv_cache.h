@@ -52,7 +52,8 @@ extern "C" {
 #define DCKV_ROPE_PARTS 3       /* f_i * (w + (1 - w) / factor) with
                                    w = clamp((t - low) / (high - low), 0, 1) and
                                    t = original_len f_i / (2 pi), the turns that pair i makes
-                                   within the trained length                               */
+                                   within the trained length (the ramp is linear in turns; one
+                                   linear in i gives other frequencies: fill freq by hand) */
 #define DCKV_ROPE_FORWARD 0     /* a' = m (a cos - b sin),  b' = m (b cos + a sin)         */
 #define DCKV_ROPE_GRADIENT 1    /* its transpose: a' = m (a cos + b sin), b' = m (b cos - a sin);
                                    the gradient of x from the gradient of the output       */
@@ -116,7 +117,8 @@ typedef struct {
  * sequence and their outputs are left as they were. */
 typedef struct {
   int32_t batch;      /* 1 .. DCKV_MAX_PROMPTS                                             */
-  int32_t max_new;    /* host bound of n_b, 1 .. 2^30 (DCKV_ERANGE where n_b is larger)    */
+  int32_t max_new;    /* host bound of n_b, 1 .. 2^30 (DCKV_ERANGE where n_b is larger); attention
+                         looks at row tiles up to it, so a far larger one costs time        */
   int32_t max_pages;  /* columns of page_table                                             */
   int32_t reserved;   /* 0                                                                 */
   const int32_t *offsets;    /* device [batch + 1], non-decreasing                         */
@@ -131,8 +133,8 @@ typedef struct {
  * rotated (forward) on their way, at position positions[token] or, where positions (device
  * int32 [n_tokens]) is NULL, at their slot; without it they are copied.  With q (device
  * [n_tokens][n_q_heads][head_dim], needs rope), q is rotated at the same position into q_out,
- * which may be q itself with its strides, or must not overlap it.  k, v and q must not overlap
- * the pools, and two tokens of one call must not share a slot.  With n_b = kv_lens[b] and no rope
+ * which may be q itself with its strides, or must not overlap it.  k, v, q and q_out must not
+ * overlap the pools nor q_out k and v, and two tokens of one call must not share a slot.  With n_b = kv_lens[b] and no rope
  * this takes over what dckv_decode wrote: layer stride n_tokens * 512, token stride 512, head
  * stride 256. */
 typedef struct {
@@ -173,6 +175,9 @@ int dckv_cache_rows(const dckv_kv_pool *pool, const dckv_cache_batch *batch, con
  * Scores, maxima, sums and outputs are fp32; the weights are rounded to the cache's type before
  * they multiply v (by at most half a step of each weight; in fp16 a weight below 2^-21 of the row's
  * largest by at most 2^-32 of that one), and out is rounded once.
+ * One kernel serves a whole call, chosen by max_new times g: single tokens that share a call with a
+ * long chunk run on its 256-row tiles, so a caller that has both gains by two calls (up to 1.45
+ * times on 63 tokens beside a chunk of 512 at dim 64, 1.05 times at dim 256).
  * For a given device and arguments, the result is the same on every call; a sequence's bits
  * may depend on the other sequences of the call, which decide where its slots are split. */
 typedef struct {

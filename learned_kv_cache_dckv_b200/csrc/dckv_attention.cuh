@@ -1159,7 +1159,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           const uint64_t scale2 = f2(a.scale_log2, a.scale_log2), off2 = f2(off, off);
           // Packed multiply-adds: 408 -> 396 us on 2,048 tokens over 32,768 slots.  Taking every second
           // to fourth pair's exp2 off the special-function unit (a polynomial on the FMA pipe) made
-          // dim 128 slower, 415 -> 428-451 us: instruction issue bounds this phase, not that unit.
+          // dim 128 slower, 415 -> 428-451 us.  Neither that unit (44% busy at dim 64, 42% at 128) nor
+          // instruction issue (28%, 27%) bounds the smaller dims: it is the latency of one tile's chain,
+          // wait for S - load - maximum - exchange - exp2 - store - signal, with two softmax warps per
+          // scheduler and S(j + 1) queued behind O(j - 1), whose P lies in its columns.
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float2 y = un2(fma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, off2));
@@ -1251,7 +1254,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_few(const AttnDev a, int 
   constexpr int V = E >= 4 ? 4 : E;
   __shared__ float acc_sm[JOIN_WARPS][D];
   __shared__ float2 ml_sm[JOIN_WARPS];
-  wait_chained();  // launched while the parts are still written
+  wait_chained();  // the parts are complete
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 ds = a.desc[2 * c];
   if (ds.x < 0) return;
@@ -1388,7 +1391,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_many(const AttnDev a, int
   constexpr int CHUNKS = D / 16 / JOIN_STEPS;
   __shared__ float4 acc_sm[JOIN_WARPS][JOIN_STEPS][32];
   __shared__ float2 ml_sm[JOIN_WARPS][32];
-  wait_chained();  // launched while the parts are still written
+  wait_chained();  // the parts are complete
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 3;
   const int4 ds = a.desc[2 * c];
   if (ds.x < 0) return;
@@ -1463,7 +1466,9 @@ static AttnLayout attn_layout(int rows, int dim) {  // rows: 8, 16 or PAIR_ROWS
 // else a pair's 256 (k_attend_many).  Measured on 64 ragged sequences of up to 8,192 slots, few / many:
 // dim 256, 8 rows 117 / 133 us, 16 rows 160 / 135; dim 128, 8 rows 75 / 112, 16 rows 88 / 110, 24 rows
 // (two tiles of 16 at dim 256: 200) many 106; dim 64, 16 rows 72 / 106.  One sequence of 1,000 slots:
-// the same within 1 us.  A group of more than 128 heads does not fit a CTA's rows and takes the few
+// the same within 1 us.  One sequence's chunk sends the whole call to the pairs: 63 single tokens beside
+// 512 tokens, 4,096 to 7,939 slots each, 8 heads, 139 / 144 / 189 us at dim 64 / 128 / 256, in two calls
+// 96 / 117 / 181.  A group of more than 128 heads does not fit a CTA's rows and takes the few
 // rows' tiles, several per token.
 static int attn_rows(const BatchDev &b, int group, int dim) {
   const int64_t rows = (int64_t)b.max_new * group;

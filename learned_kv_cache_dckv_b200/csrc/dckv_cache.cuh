@@ -10,9 +10,13 @@
 // pairs (half layout) or V whole pairs (interleaved layout).
 // Blocks are small (128 threads) where there are many, so that some blocks' loads cover others'
 // look-ups.  Measured on four 4,096-token prompts, six layers, 207 MB (appended without a rotation)
-// and 258 MB (rows): 128 threads 41 and 53 us; 256 threads 45 and 59; a thread per chunk (384) 62
-// and 83; first chunk loaded before the look-up 48 and 58; four chunks ahead per thread 63 and 88;
-// four tokens per block 44-52 and 56-63; blocks of one layer's keys or values 53-65 and 111-119.
+// and 258 MB (rows), before evict-first loads and chained launches (38 and 49 us with them): 128
+// threads 41 and 53 us; 256 threads 45 and 59; a thread per chunk (384) 62 and 83; first chunk loaded
+// before the look-up 48 and 58; four chunks ahead per thread 63 and 88; four tokens per block 44-52 and
+// 56-63; blocks of one layer's keys or values 53-65 and 111-119.  These shapes were not measured on
+// k_rope (4,096 tokens x 8 heads x 256 in bf16 10.5 us, 49% of the copy rate): the lanes of a
+// head read their (cos, sin) pairs 64 bytes apart, eight addresses to a bank, and the loads of x wait
+// for the angles.
 #pragma once
 #include "../../include/dckv_cache.h"
 #include "dckv_epilogues.cuh"
