@@ -135,8 +135,8 @@ typedef struct {
  * [n_tokens][n_q_heads][head_dim], needs rope), q is rotated at the same position into q_out,
  * which may be q itself with its strides, or must not overlap it.  k, v, q and q_out must not
  * overlap the pools, nor q_out k and v, and two tokens of one call must not share a slot.  With
- * n_b = kv_lens[b] and no rope this takes over what dckv_decode wrote: layer stride n_tokens * 512, token stride 512, head
- * stride 256. */
+ * n_b = kv_lens[b] and no rope this takes over what dckv_decode wrote: layer stride
+ * n_tokens * 512, token stride 512, head stride 256. */
 typedef struct {
   const void *k, *v;
   int64_t k_layer_stride, k_token_stride, k_head_stride;

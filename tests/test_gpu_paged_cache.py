@@ -1,13 +1,12 @@
 """PagedCache and the calls behind it on a GPU, against oracle/cache.py (fp64).  Tolerances as in
 test_gpu_cache.py; a row that was rotated on its way in and back on its way out has both passes'
 errors, the first one's turned (a pair's |a| + |b| grows by at most 2 in the turn)."""
-import numpy as np
 import pytest
 import torch
 
 import learned_kv_cache_dckv_b200 as D
 import oracle.cache as OC
-from test_gpu_cache import BF16, FP16, Paged, attend, check_attention, ints, normal, rope_tol, status, u, within
+from test_gpu_cache import BF16, FP16, Paged, ints, normal, rope_tol, status, u, within
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +98,32 @@ def test_append_layer_by_layer(dtype, heads, dim):
         assert torch.equal(caches[0].k[:, pages, rows], caches[1].k[:, pages, rows])
         assert torch.equal(caches[0].v[:, pages, rows], caches[1].v[:, pages, rows])
     assert int(caches[0].status) == 0 and int(caches[1].status) == 0
+
+
+def test_a_captured_step_outlives_larger_calls():
+    """A graph of a single token's step is replayed after a chunk has needed a larger workspace and
+    other tensors have taken what memory was free."""
+    cache = D.PagedCache(200, page_size=32, n_layers=1)
+    a, b = cache.add(), cache.add()
+    k, v = normal(1, 1, 5000, 2, 256), normal(2, 1, 5000, 2, 256)
+    cache.append(cache.extend([a, b], [4000, 1000]), k, v)
+    step = cache.extend([a, b], [1, 1])
+    cache.append(step, k[:, :2], v[:, :2])
+    q, out = normal(3, 2, 8, 256), torch.empty(2, 8, 256, dtype=BF16, device="cuda")
+    want = cache.attend(0, step, q).clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.attend(0, step, q, out=out)
+    chunk = cache.extend([b], [64])
+    cache.append(chunk, k[:, :64], v[:, :64])
+    q2 = normal(4, 64, 8, 256)
+    want2 = cache.attend(0, chunk, q2).clone()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    assert torch.equal(cache.attend(0, chunk, q2), want2)
+    assert all(bool((t == 7).all()) for t in others) and int(cache.status) == 0
